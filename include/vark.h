@@ -536,6 +536,141 @@ int vark_pruned_attention_int3(const uint16_t* q, const uint8_t* kq, const uint8
                                const float* tau, const float* bias,
                                uint16_t* out, int32_t* dev_status, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Serving: a paged cache.  The calls above lay a cache out in advance for one
+ * batch whose members are at the same scale; these serve sequences of any
+ * lengths side by side (prompts in chunks, one token at a time, drafted tokens,
+ * a new scale), their rows scattered over pages of one pool.
+ *
+ * Element types: `dtype` is VARK_BF16 or VARK_FP16 for every 16-bit tensor of a
+ *   call (raw bits in uint16_t); sums, maxima and norms are fp32 and a value is
+ *   rounded once, when it is stored (attention rounds its probabilities to
+ *   dtype as well, as the calls above do).
+ * Chunk: the new tokens of all sequences one behind another; cu_tokens (dev
+ *   int32 [B + 1], ascending from 0) gives their bounds, sequence b holding
+ *   tokens cu_tokens[b] .. cu_tokens[b + 1] - 1, possibly none.  Tokens from
+ *   cu_tokens[B] on are padding: not read, and their outputs not written.
+ * Pool: k_pages, v_pages dev [n_pages][H][page_size][D], page_size 16, 32, 64,
+ *   128 or 256.  With head_pages = 1 a page holds rows of a single head,
+ *   [n_pages][page_size][D], and every (sequence, head) has its own list and
+ *   length: what a head-scale keep schedule leaves, where head h holds
+ *   past_len[h][k] retained rows (vark_build_offsets) before scale k.
+ * Table: page_table dev int32 [B][max_pages] (head_pages: [B][H][max_pages]);
+ *   row r of a sequence is row r % page_size of page page_table[b][r /
+ *   page_size].  Entries behind a sequence's last row are not read.
+ * Length: cache_len dev int32 [B] (head_pages: [B][H]): rows with the chunk's
+ *   tokens among them, so token i of the n tokens of b is row cache_len - n + i
+ *   for the append and the attention alike.  A length below n holds only the
+ *   last cache_len tokens of the chunk.
+ * Sequences may share pages that are only read; the rows of one append must be
+ * distinct.  Tables that leave the arguments' ranges (offsets outside
+ * [0, n_tokens] or descending, cache_len outside [0, max_pages * page_size], a
+ * page in use outside [0, n_pages), a position behind the rotation table) set
+ * *dev_status to VARK_E_SHAPE; nothing outside the arguments is touched, the
+ * rows concerned are not stored (norm, append), the attention's outputs are
+ * unspecified.
+ * Every call can be captured into a CUDA graph: lengths, tables and positions
+ * are read when it runs.
+ * ------------------------------------------------------------------------- */
+enum vark_dtype { VARK_BF16 = 0, VARK_FP16 = 1 };
+enum vark_norm {
+  VARK_NORM_NONE = 0,
+  VARK_NORM_RMS = 1,    /* x / sqrt(mean(x^2) + eps) */
+  VARK_NORM_L2 = 2      /* x / max(||x||, eps): the unit-length queries and keys
+                           that a learned temperature tau goes with */
+};
+
+/*
+ * vark_qk_norm_rope -- device.  Norm of every query and key row (per head, over
+ * its D channels), times the weight, and the position rotation, in one pass.
+ *   q, k         dev 16-bit rows; the row of (b, t, h) starts at b * strides[0]
+ *                + t * strides[1] + h * strides[2] (host int64 [3], elements,
+ *                multiples of 8, >= 0, not looked at on an axis of one entry; D
+ *                channels contiguous), so a slice of a fused projection is
+ *                read, and the [B][H][T][D] of the dense attention calls
+ *                written, in place.  Either may be NULL (with its strides,
+ *                output and weight).
+ *   q_out, k_out dev, by their own strides; may be q, k themselves (same
+ *                strides), else they must not overlap the inputs.
+ *   B, T         >= 0;  Hq, Hk >= 1;  D 64 or 128.
+ *   norm         vark_norm;  eps >= 0.
+ *   q_weight, k_weight  dev fp32 [D], or NULL for ones.
+ *   rope         dev fp32 [rope_len][2][rope_dim / 2]: a position's cosines,
+ *                then its sines (any angles: one axis, or the 2-D angles of a
+ *                scale's tokens), or NULL for no rotation.  Channels from
+ *                rope_dim on are not rotated; rope_dim a multiple of 16, <= D.
+ *   pairs        0: channel j turns with j + rope_dim / 2;  1: 2j with 2j + 1.
+ *                (a, b) becomes (a cos_j - b sin_j, a sin_j + b cos_j).
+ *   positions    dev int32 [B][T], given exactly when rope is; a token whose
+ *                position is negative is padding: its outputs are not written.
+ * The squares of a row are summed in fp32: rows whose norm passes 1.8e19
+ *   (bf16 only) overflow.
+ * Errors: VARK_E_ARG, VARK_E_SHAPE, VARK_E_ALIGN, VARK_E_CUDA, VARK_E_DEVICE.
+ */
+int vark_qk_norm_rope(int dtype, const uint16_t* q, const int64_t* q_strides, uint16_t* q_out,
+                      const int64_t* q_out_strides, int Hq, const uint16_t* k, const int64_t* k_strides,
+                      uint16_t* k_out, const int64_t* k_out_strides, int Hk, int B, int T, int D, int norm,
+                      const float* q_weight, const float* k_weight, float eps, const float* rope, int rope_len,
+                      int rope_dim, int pairs, const int32_t* positions, int32_t* dev_status, void* stream);
+
+/*
+ * vark_paged_append -- device.  Writes a chunk's keys, normed and rotated on the
+ * way as by vark_qk_norm_rope, and its values, as they are, to their rows of
+ * the paged cache (see above).
+ *   k, v         dev 16-bit; the row of (token, head) starts at token *
+ *                strides[0] + head * strides[1] (host int64 [2], elements,
+ *                multiples of 8, >= 0).
+ *   n_tokens     tokens of the chunk, padding included;  H kv heads.
+ *   positions    dev int32 [n_tokens], given exactly when rope is; tokens with
+ *                a negative position are not stored.
+ *   other arguments as above and as vark_qk_norm_rope.
+ * Errors: as vark_qk_norm_rope.
+ */
+int vark_paged_append(int dtype, const uint16_t* k, const int64_t* k_strides, const uint16_t* v,
+                      const int64_t* v_strides, int64_t n_tokens, int B, int H, int D, const int32_t* cu_tokens,
+                      uint16_t* k_pages, uint16_t* v_pages, int64_t n_pages, int page_size,
+                      const int32_t* page_table, int max_pages, const int32_t* cache_len, int head_pages, int norm,
+                      const float* k_weight, float eps, const float* rope, int rope_len, int rope_dim, int pairs,
+                      const int32_t* positions, int32_t* dev_status, void* stream);
+
+/*
+ * vark_paged_attention_workspace -- host.  Bytes of workspace that
+ * vark_paged_attention wants for these shapes (> 0), or a negative status.
+ */
+int64_t vark_paged_attention_workspace(int64_t n_tokens, int B, int Hq, int Hkv, int D, int page_size,
+                                       int max_pages);
+
+/*
+ * vark_paged_attention -- device.  Attention of a chunk's queries over the paged
+ * cache, the chunk's own keys among its rows (append first).  Query head h
+ * reads kv head h / (Hq / Hkv).  Token i of a sequence's n tokens sees
+ *   causal = 1   rows 0 .. cache_len - n + i (language-model chunks, decoding
+ *                at n = 1, drafted tokens);
+ *   causal = 0   every row (a new scale, whose tokens all see one another).
+ * Logit tau[h] * (q . k) / sqrt(D); softmax over the rows seen.  A query that
+ * sees no row gets a zero output and -inf in lse.
+ *   q, out       dev 16-bit; the row of (token, head) starts at token *
+ *                strides[0] + head * strides[1] (as vark_paged_append).
+ *   tau          dev fp32 [Hq] or NULL (ones).
+ *   lse          dev fp32 [n_tokens][Hq] out, or NULL: log of the sum of exp of
+ *                the logits, with which outputs over disjoint caches combine.
+ *   workspace    dev, vark_paged_attention_workspace bytes, 16-byte aligned;
+ *                holds nothing between calls.  Calls that may run at the same
+ *                time need one each; a stream's calls can share one.
+ * Rows behind cache_len may hold anything.  The rows of a cache that some query
+ *   of the chunk sees must hold finite values (another query that does not see
+ *   a NaN or infinity may still be reached by it).
+ * Limits: n_tokens * Hq < 2^30, B * Hkv <= 2^24.
+ * Errors: VARK_E_ARG, VARK_E_SHAPE, VARK_E_ALIGN, VARK_E_CUDA, VARK_E_DEVICE;
+ *   *dev_status as vark_scas_accumulate, and the tables' VARK_E_SHAPE.
+ */
+int vark_paged_attention(int dtype, const uint16_t* q, const int64_t* q_strides, int64_t n_tokens, int B, int Hq,
+                         int Hkv, int D, const int32_t* cu_tokens, const uint16_t* k_pages,
+                         const uint16_t* v_pages, int64_t n_pages, int page_size, const int32_t* page_table,
+                         int max_pages, const int32_t* cache_len, int head_pages, const float* tau, int causal,
+                         uint16_t* out, const int64_t* out_strides, float* lse, void* workspace,
+                         int64_t workspace_bytes, int32_t* dev_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,6 +22,10 @@ VARK_OK = 0
 STATUS_NAMES = {0: "VARK_OK", -1: "VARK_E_ARG", -2: "VARK_E_SHAPE", -3: "VARK_E_ALIGN", -4: "VARK_E_BUDGET",
                 -5: "VARK_E_CUDA", -6: "VARK_E_TIMEOUT", -7: "VARK_E_DEVICE"}
 
+# vark_dtype, vark_norm
+VARK_BF16, VARK_FP16 = 0, 1
+VARK_NORM_NONE, VARK_NORM_RMS, VARK_NORM_L2 = 0, 1, 2
+
 _lib = None
 
 
@@ -36,6 +40,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
 _U32 = ctypes.c_uint32
+_F = ctypes.c_float
 
 _SIGNATURES = {
     "vark_status_string": (ctypes.c_char_p, [_I]),
@@ -66,6 +71,13 @@ _SIGNATURES = {
                                         _P, _P, _P, _P]),
     "vark_pruned_attention_int3": (_I, [_P, _P, _P, _P, _P, _I64, _P, _P, _I, _I, _I, _I, _P, _I, _P, _P, _P, _P,
                                         _P, _P, _P, _P]),
+    "vark_qk_norm_rope": (_I, [_I, _P, _P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _F, _P, _I, _I,
+                               _I, _P, _P, _P]),
+    "vark_paged_append": (_I, [_I, _P, _P, _P, _P, _I64, _I, _I, _I, _P, _P, _P, _I64, _I, _P, _I, _P, _I, _I, _P,
+                               _F, _P, _I, _I, _I, _P, _P, _P]),
+    "vark_paged_attention_workspace": (_I64, [_I64, _I, _I, _I, _I, _I, _I]),
+    "vark_paged_attention": (_I, [_I, _P, _P, _I64, _I, _I, _I, _I, _P, _P, _P, _I64, _I, _P, _I, _P, _I, _P, _I,
+                                  _P, _P, _P, _P, _I64, _P, _P]),
 }
 
 
@@ -588,3 +600,230 @@ def vark_pruned_attention_int3(q, kq, vq, k_scale, v_scale, kc_rows: int, k_dens
     """Device: pruned attention of one layer straight over its 3-bit codes (D = 128)."""
     _pruned_packed(3, q, kq, vq, k_scale, v_scale, kc_rows, k_dense, v_dense, sides, query_scale, head_off,
                    seg_off, past_len, tau, bias, out, dev_status, stream)
+
+
+# ------------------------------------------------------------------ paged cache
+_I64x2, _I64x3 = _I64 * 2, _I64 * 3
+
+
+def _paged_dtype(t, name):
+    torch = _torch()
+    if t.dtype is torch.bfloat16:
+        return VARK_BF16
+    if t.dtype is torch.float16:
+        return VARK_FP16
+    raise TypeError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
+
+
+def _pointers(dev, specs):
+    """Device pointers of (tensor or None, name, dtype, shape, rows) in order.
+    rows: 0 for a contiguous tensor, else rows of contiguous channels with any
+    other strides (1 read, 2 written).  The small calls cost more on the host
+    than on the device, so a tensor is tested in one expression and a refusal
+    looked into apart (one call per check and tensor measured 10 us more)."""
+    if dev < 0:
+        _refuse(dev, specs)
+    out = []
+    for t, _, dtype, shape, rows in specs:
+        if t is None:
+            out.append(None)
+            continue
+        if (t.shape != shape or t.dtype is not dtype or t.get_device() != dev
+                or not (t.is_contiguous() or (rows and _strides_fit(t, rows)))):
+            _refuse(dev, specs)
+        out.append(t.data_ptr())
+    return out
+
+
+def _strides_fit(t, rows):
+    st, shape = t.stride(), t.shape
+    if st[-1] != 1:
+        return False
+    # an output's rows must not overlap (an axis of one entry has no step)
+    return rows == 1 or all(n <= 1 or s >= shape[-1] for n, s in zip(shape[:-1], st[:-1]))
+
+
+def _refuse(dev, specs):
+    for t, name, _, shape, _ in specs:
+        if t is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    for t, name, dtype, shape, rows in specs:
+        if t is None:
+            continue
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, the call on cuda:{dev}")
+        if rows and not (t.is_contiguous() or _strides_fit(t, rows)):
+            raise ValueError(f"{name}: the channels must be contiguous, and an output's rows distinct")
+        if not rows and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    raise ValueError("tensor arguments")
+
+
+def _call_on(dev, stream, fn, *args):
+    """fn(*args, stream) with the tensors' device current."""
+    cuda = _torch().cuda
+    if cuda.current_device() == dev:
+        # (looking the device up again inside current_stream would cost 3 us)
+        return fn(*args, _torch()._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    with cuda.device(dev):
+        return fn(*args, _stream(stream))
+
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+_torch_module = None
+
+
+def _rank(t, n, name):
+    """The shape of a tensor of n axes."""
+    shape = t.shape
+    if len(shape) != n:
+        raise ValueError(f"{name} must have {n} dimensions")
+    return shape
+
+
+def _rope_dims(rope, positions):
+    if (rope is None) != (positions is None):
+        raise ValueError("rope and positions come together")
+    if rope is None:
+        return None, 0, 0
+    shape = n, two, half = _rank(rope, 3, "rope")
+    if two != 2:
+        raise ValueError(f"rope: shape {tuple(shape)}, expected [positions][2][rope_dim / 2]")
+    return shape, n, 2 * half
+
+
+def _status_spec(dev_status, i32):
+    if dev_status is None or dev_status.numel() < 1:
+        raise ValueError("dev_status: at least one element is needed")
+    return (dev_status, "dev_status", i32, dev_status.shape, 0)
+
+
+def vark_qk_norm_rope(q, k, q_out, k_out, norm: int, q_weight, k_weight, eps: float, rope, positions, dev_status,
+                      pairs: bool = False, stream=None):
+    """Device: norm per head and position rotation of queries and keys in one
+    pass (see vark.h).  q [B][T][Hq][D] and k [B][T][Hk][D] bf16 or fp16 with
+    any strides but the channels', outputs alike; either may be None (its
+    output and weight then too); weights fp32 [D] or None; rope fp32
+    [positions][2][rope_dim / 2] and positions int32 [B][T], or both None."""
+    torch = _torch()
+    f32, i32 = torch.float32, torch.int32
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q or k is required")
+    B, T, _, D = _rank(x, 4, "q" if q is not None else "k")
+    dt, dtype = _paged_dtype(x, "q"), x.dtype
+    rope_shape, rope_len, rope_dim = _rope_dims(rope, positions)
+    q_shape = k_shape = None
+    Hq = Hk = 0
+    if q is not None:
+        Hq = _rank(q, 4, "q")[2]
+        q_shape = (B, T, Hq, D)
+    if k is not None:
+        Hk = _rank(k, 4, "k")[2]
+        k_shape = (B, T, Hk, D)
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None) or (
+            q is None and q_weight is not None) or (k is None and k_weight is not None):
+        raise ValueError("q, q_out and q_weight come together, as do k, k_out and k_weight")
+    pq, pqo, pqw, pk, pko, pkw, pr, pp, ps = _pointers(x.get_device(), (
+        (q, "q", dtype, q_shape, 1), (q_out, "q_out", dtype, q_shape, 2), (q_weight, "q_weight", f32, (D,), 0),
+        (k, "k", dtype, k_shape, 1), (k_out, "k_out", dtype, k_shape, 2), (k_weight, "k_weight", f32, (D,), 0),
+        (rope, "rope", f32, rope_shape, 0), (positions, "positions", i32, (B, T), 0), _status_spec(dev_status, i32)))
+    _check(_call_on(x.get_device(), stream, _load().vark_qk_norm_rope, dt,
+                    pq, None if q is None else _I64x3(*q.stride()[:3]),
+                    pqo, None if q is None else _I64x3(*q_out.stride()[:3]), Hq,
+                    pk, None if k is None else _I64x3(*k.stride()[:3]),
+                    pko, None if k is None else _I64x3(*k_out.stride()[:3]), Hk,
+                    B, T, D, norm, pqw, pkw, eps, pr, rope_len, rope_dim, 1 if pairs else 0, pp, ps),
+           "vark_qk_norm_rope")
+
+
+def _page_specs(k_pages, v_pages, page_table, cache_len, cu_tokens, dtype, H, D):
+    """What the append and the attention share: specs of the pool, tables and
+    lengths, and (n_pages, page_size, max_pages, head_pages, B)."""
+    B = cu_tokens.numel() - 1
+    if B < 0:
+        raise ValueError("cu_tokens needs at least one entry")
+    head_pages = len(k_pages.shape) == 3
+    if head_pages:
+        n_pages, page_size, _ = k_pages.shape
+        pool, seqs = (n_pages, page_size, D), (B, H)
+    else:
+        n_pages, _, page_size, _ = _rank(k_pages, 4, "k_pages")
+        pool, seqs = (n_pages, H, page_size, D), (B,)
+    if len(page_table.shape) != len(seqs) + 1:
+        raise ValueError(f"page_table: shape {tuple(page_table.shape)}, expected {(*seqs, 'max_pages')}")
+    max_pages = page_table.shape[-1]
+    i32 = _torch().int32
+    specs = [(k_pages, "k_pages", dtype, pool, 0), (v_pages, "v_pages", dtype, pool, 0),
+             (page_table, "page_table", i32, (*seqs, max_pages), 0), (cache_len, "cache_len", i32, seqs, 0),
+             (cu_tokens, "cu_tokens", i32, (B + 1,), 0)]
+    return specs, n_pages, page_size, max_pages, 1 if head_pages else 0, B
+
+
+def vark_paged_append(k, v, cu_tokens, k_pages, v_pages, page_table, cache_len, norm: int, k_weight, eps: float,
+                      rope, positions, dev_status, pairs: bool = False, stream=None):
+    """Device: a chunk's keys (normed and rotated on the way) and values into
+    the paged cache (see vark.h).  k, v [tokens][H][D] bf16 or fp16 with any
+    strides but the channels'; pools [pages][H][page_size][D] with page_table
+    [B][max_pages] and cache_len [B], or head-specific pools
+    [pages][page_size][D] with [B][H][max_pages] and [B][H]; cu_tokens int32
+    [B + 1]; rope and positions (int32 [tokens]) as vark_qk_norm_rope."""
+    torch = _torch()
+    shape = n, H, D = _rank(k, 3, "k")
+    dt = _paged_dtype(k, "k")
+    rope_shape, rope_len, rope_dim = _rope_dims(rope, positions)
+    specs, n_pages, page_size, max_pages, head_pages, B = _page_specs(k_pages, v_pages, page_table, cache_len,
+                                                                      cu_tokens, k.dtype, H, D)
+    specs += [(k, "k", k.dtype, shape, 1), (v, "v", k.dtype, shape, 1), (k_weight, "k_weight", torch.float32, (D,), 0),
+              (rope, "rope", torch.float32, rope_shape, 0), (positions, "positions", torch.int32, (n,), 0),
+              _status_spec(dev_status, torch.int32)]
+    dev = k.get_device()
+    kp, vp, tp, lp, cp, pk, pv, pw, pr, pp, ps = _pointers(dev, specs)
+    _check(_call_on(dev, stream, _load().vark_paged_append, dt, pk, _I64x2(*k.stride()[:2]), pv, _I64x2(*v.stride()[:2]), n, B,
+                    H, D, cp, kp, vp, n_pages, page_size, tp, max_pages, lp, head_pages, norm, pw, eps, pr, rope_len,
+                    rope_dim, 1 if pairs else 0, pp, ps), "vark_paged_append")
+
+
+def vark_paged_attention_workspace(n_tokens: int, batch: int, q_heads: int, kv_heads: int, D: int, page_size: int,
+                                   max_pages: int) -> int:
+    """Host: bytes of workspace for vark_paged_attention at these shapes."""
+    n = int(_load().vark_paged_attention_workspace(int(n_tokens), int(batch), int(q_heads), int(kv_heads), int(D),
+                                                   int(page_size), int(max_pages)))
+    if n < 0:
+        raise VarkError(n, "vark_paged_attention_workspace")
+    return n
+
+
+def vark_paged_attention(q, cu_tokens, k_pages, v_pages, page_table, cache_len, tau, causal: bool, out, lse,
+                         workspace, dev_status, stream=None):
+    """Device: attention of a chunk's queries over the paged cache (see vark.h).
+    q, out [tokens][Hq][D] with any strides but the channels'; pools, tables and
+    lengths as vark_paged_append; tau fp32 [Hq] or None; lse fp32 [tokens][Hq]
+    or None; workspace uint8 of vark_paged_attention_workspace bytes."""
+    torch = _torch()
+    shape = n, Hq, D = _rank(q, 3, "q")
+    dt = _paged_dtype(q, "q")
+    H = page_table.shape[1] if len(k_pages.shape) == 3 else k_pages.shape[1]
+    if H < 1 or Hq % H:
+        raise ValueError(f"{Hq} query heads over {H} kv heads")
+    specs, n_pages, page_size, max_pages, head_pages, B = _page_specs(k_pages, v_pages, page_table, cache_len,
+                                                                      cu_tokens, q.dtype, H, D)
+    specs += [(q, "q", q.dtype, shape, 1), (out, "out", q.dtype, shape, 2), (tau, "tau", torch.float32, (Hq,), 0),
+              (lse, "lse", torch.float32, (n, Hq), 0), (workspace, "workspace", torch.uint8, workspace.shape, 0),
+              _status_spec(dev_status, torch.int32)]
+    dev = q.get_device()
+    kp, vp, tp, lp, cp, pq, po, pt, pl, pw, ps = _pointers(dev, specs)
+    _check(_call_on(dev, stream, _load().vark_paged_attention, dt, pq, _I64x2(*q.stride()[:2]), n, B, Hq, H, D, cp, kp, vp,
+                    n_pages, page_size, tp, max_pages, lp, head_pages, pt, 1 if causal else 0, po,
+                    _I64x2(*out.stride()[:2]), pl, pw, workspace.numel(), ps), "vark_paged_attention")

@@ -1,0 +1,688 @@
+// Attention of a chunk of new tokens over a paged cache (vark_paged_attention).
+//
+// Mathematics: query row i of head h sees keys j < lim_i; with x_j = tau[h]
+// (q_i . k_j) / sqrt(D) the output is sum_j 2^(x'_j - m) v_j / l, x' = x log2 e,
+// m the running maximum and l = sum_j 2^(x'_j - m): one pass over the keys.
+//
+// The G query heads of a kv head share its keys, so the G * n rows of a
+// sequence's n tokens (token-major: row = token * G + head) are cut into tiles
+// of R rows: an item is (sequence, kv head, row tile).  Work is split along the
+// keys as well: all items' key tiles are laid end to end and every CTA takes an
+// equal share of them, so one long cache spreads over the whole device and a
+// ragged batch leaves no CTA with the longest sequence.  An item that falls
+// into several shares leaves one partial (o, m, l) per CTA in the workspace; a
+// second, small kernel joins them.  Lengths live on the device: every CTA
+// finds its share with one scan over the sequence table.
+#include <cstdlib>
+
+#include "vark_paged.cuh"
+
+namespace vark {
+namespace paged {
+
+constexpr int kCtas = 148;             // one persistent CTA per SM
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescale = 8.0f;       // log2: a running maximum may lag by this much
+
+struct AttnParams {
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;              // [N][Hq] or null
+  int64_t qs[2], os[2];    // token, head strides (elements)
+  Pages pg;
+  const int32_t* cu;       // [B + 1]
+  const float* tau;        // [Hq] or null
+  int64_t N;
+  int B, G, Hq, causal;
+  float scale_log2;        // log2(e) / sqrt(D)
+  float* part_o;           // [kCtas][2][R][D]
+  float* part_ml;          // [kCtas][2][R][2]
+  int32_t* status;
+  uint64_t wait_limit_ns;
+  int withhold;            // test hook: slices a warp loads before it stops (-1: all)
+};
+
+// ------------------------------------------------------------------ the plan
+// An entry is one row of the length table: a sequence (shared pages, all kv
+// heads) or a (sequence, head).
+struct Entry {
+  int first, n;            // first token, tokens
+  int len;                 // cache rows
+  int row_tiles, key_tiles;
+  int items;               // kv heads of the entry * row_tiles
+};
+
+// Lengths and token offsets that do not fit the arguments leave the entry
+// without work and are recorded.
+template <int R, int KT>
+VARK_DEV Entry load_entry(const AttnParams& p, int e) {
+  Entry x;
+  const int b = e / p.pg.table_heads;
+  x.first = p.cu[b];
+  const int end = p.cu[b + 1];
+  x.len = p.pg.len[e];
+  if (x.first < 0 || end < x.first || end > p.N || x.len < 0 || (x.len - 1) >> p.pg.log2_page >= p.pg.max_pages) {
+    record(p.status, VARK_E_SHAPE);
+    x.first = x.n = x.len = 0;
+  } else {
+    x.n = end - x.first;
+  }
+  x.row_tiles = (x.n * p.G + R - 1) / R;
+  x.key_tiles = max(1, (x.len + KT - 1) / KT);
+  x.items = x.row_tiles * (p.pg.table_heads > 1 ? 1 : p.pg.heads);
+  return x;
+}
+
+struct Share {
+  int64_t total;           // units (key tiles) of the call
+  int64_t u0, u1;          // this CTA's units
+  int e;                   // entry of the unit asked for, and its first unit
+  int64_t base;
+};
+
+VARK_DEV int64_t share_begin(int64_t total, int ctas, int c) { return total * c / ctas; }
+
+// Scan over the entries by the whole block: the share of CTA `cta`, and the
+// entry that holds its first (LAST = false) or last unit.
+template <int R, int KT, int THREADS, bool LAST>
+VARK_DEV Share find_share(const AttnParams& p, int cta) {
+  __shared__ int64_t warp_sum[THREADS / 32];
+  __shared__ int64_t found_base;
+  __shared__ int found_e;
+  const int E = p.B * p.pg.table_heads;
+  const int chunk = (E + THREADS - 1) / THREADS;
+  const int e0 = min(E, int(threadIdx.x) * chunk), e1 = min(E, e0 + chunk);
+  int64_t sum = 0;
+  for (int e = e0; e < e1; ++e) {
+    const Entry x = load_entry<R, KT>(p, e);
+    sum += int64_t(x.items) * x.key_tiles;
+  }
+  int64_t incl = sum;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  Share s;
+  s.total = 0;
+  int64_t before = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += warp_sum[w];
+    s.total += warp_sum[w];
+  }
+  const int ctas = int(min(int64_t(kCtas), s.total));
+  s.e = 0;
+  s.base = s.u0 = s.u1 = 0;
+  if (cta >= ctas) return s;     // the same for every thread
+  s.u0 = share_begin(s.total, ctas, cta);
+  s.u1 = share_begin(s.total, ctas, cta + 1);
+  const int64_t want = LAST ? s.u1 - 1 : s.u0;
+  int64_t base = before + incl - sum;
+  if (want >= base && want < base + sum) {
+    for (int e = e0; e < e1; ++e) {
+      const Entry x = load_entry<R, KT>(p, e);
+      const int64_t w = int64_t(x.items) * x.key_tiles;
+      if (want < base + w) {
+        found_e = e;
+        found_base = base;
+        break;
+      }
+      base += w;
+    }
+  }
+  __syncthreads();
+  s.e = found_e;
+  s.base = found_base;
+  return s;
+}
+
+// A run of key tiles [k0, k1) of one item.
+template <int R, int KT>
+struct Segments {
+  int e;
+  int64_t base, u, u1;     // first unit of entry e, next unit, end of the share
+  Entry x;
+  int h, tile, k0, k1;
+
+  VARK_DEV void start(const AttnParams& p, const Share& s) {
+    e = s.e;
+    base = s.base;
+    u = s.u0;
+    u1 = s.u1;
+    if (u < u1) x = load_entry<R, KT>(p, e);
+  }
+  VARK_DEV bool next(const AttnParams& p) {
+    if (u >= u1) return false;
+    while (u >= base + int64_t(x.items) * x.key_tiles) {
+      base += int64_t(x.items) * x.key_tiles;
+      x = load_entry<R, KT>(p, ++e);
+    }
+    const int64_t off = u - base;
+    const int item = int(off / x.key_tiles);
+    k0 = int(off - int64_t(item) * x.key_tiles);
+    k1 = int(min(int64_t(x.key_tiles), k0 + (u1 - u)));
+    u += k1 - k0;
+    h = p.pg.table_heads > 1 ? e % p.pg.heads : item / x.row_tiles;
+    tile = item % x.row_tiles;
+    return true;
+  }
+  // Keys that some row of the tile sees.
+  VARK_DEV int limit(const AttnParams& p) const {
+    if (!p.causal) return x.len;
+    const int last = min(x.n - 1, (tile * R + R - 1) / p.G);
+    return max(0, x.len - x.n + last + 1);
+  }
+};
+
+struct RowAt {
+  int token, head;         // token of the batch, query head; token < 0: no such row
+  int limit;               // keys it sees
+};
+template <int R, int KT>
+VARK_DEV RowAt row_at(const AttnParams& p, const Segments<R, KT>& s, int r) {
+  RowAt a;
+  const int row = s.tile * R + r;
+  const int t = row / p.G;
+  a.head = s.h * p.G + (row - t * p.G);
+  a.token = t < s.x.n ? s.x.first + t : -1;
+  a.limit = t >= s.x.n ? 0 : p.causal ? s.x.len - s.x.n + t + 1 : s.x.len;
+  return a;
+}
+
+// Writes 8 channels of a finished row (o not yet divided by l).
+template <int DT>
+VARK_DEV void store_row8(const AttnParams& p, const RowAt& a, int d0, const float (&o)[8], float m, float l) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;    // no key: zeros
+  uint4 w;
+  w.x = pack2<DT>(o[0] * inv, o[1] * inv);
+  w.y = pack2<DT>(o[2] * inv, o[3] * inv);
+  w.z = pack2<DT>(o[4] * inv, o[5] * inv);
+  w.w = pack2<DT>(o[6] * inv, o[7] * inv);
+  *reinterpret_cast<uint4*>(p.out + a.token * p.os[0] + a.head * p.os[1] + d0) = w;
+  if (d0 == 0 && p.lse != nullptr)
+    p.lse[int64_t(a.token) * p.Hq + a.head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// ------------------------------------------------------------------ rows kernel
+// Few rows a kv head (decoding, drafted tokens): bound by reading the keys and
+// values once.  8 warps, each with a ring of its own: a warp takes every eighth
+// 16-key slice of the CTA's key tiles, loads it by TMA (a slice lies within one
+// page; 128-byte swizzle) and works on it alone -- no barrier between warps
+// until an item ends, when the 8 partial results are added in shared memory.
+constexpr int kRowWarps = 8;
+constexpr int kRowThreadsA = kRowWarps * 32;
+constexpr int kSlice = 16;
+constexpr int kRowKT = kRowWarps * kSlice;
+constexpr int kRowR = 16;
+
+template <int DT>
+VARK_DEV void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (DT == VARK_BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+VARK_DEV void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+VARK_DEV void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+template <int D>
+struct RowSmem {
+  static constexpr int kPanel = kSlice * 128;             // 16 rows x 64 channels
+  static constexpr int kHalf = (D / 64) * kPanel;         // one slice of K or V
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kRing = 0;                         // [warp][stage]
+  static constexpr int kMergeStride = D + 8;              // floats; + 8 spreads the 8 rows of a store over the banks
+  static constexpr int kMerge = kRing + kRowWarps * kStages * kStage;           // [warp][16][stride] fp32
+  static constexpr int kML = kMerge + kRowWarps * kRowR * kMergeStride * 4;    // [warp][16][2] fp32
+  static constexpr int kBar = kML + kRowWarps * kRowR * 2 * 4;
+  static constexpr int kMisc = kBar + kRowWarps * kStages * 8;
+  static constexpr int kAlloc = kMisc + 16 + 1024;
+};
+
+template <int DT, int D>
+__global__ void __launch_bounds__(kRowThreadsA, 1)
+rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+            const __grid_constant__ AttnParams p) {
+  using L = RowSmem<D>;
+  using Seg = Segments<kRowR, kRowKT>;
+  constexpr int NP = D / 64, KS = D / 16, NT = D / 8;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  float* merge = reinterpret_cast<float*>(smem + L::kMerge);
+  float* ml = reinterpret_cast<float*>(smem + L::kML);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t4 = lane & 3;
+  const uint32_t ring = sbase + L::kRing + warp * L::kStages * L::kStage;
+  const uint32_t bar0 = sbase + L::kBar + warp * L::kStages * 8;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kRowWarps * L::kStages; ++i) mbar_init(sbase + L::kBar + 8u * i, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  const Share share = find_share<kRowR, kRowKT, kRowThreadsA, false>(p, blockIdx.x);   // syncs the block
+  if (share.u0 == share.u1) return;
+
+  // The loading side of the warp: its next slice, and that slice's page.
+  Seg ps;
+  int p_slice = 0, p_end = 0, p_page = 0, p_count = 0;
+  bool p_more = true;
+  auto p_settle = [&]() {   // moves on to the next slice that exists and asks for its page
+    while (p_slice >= p_end) {
+      if (!ps.next(p)) {
+        p_more = false;
+        return;
+      }
+      p_slice = ps.k0 * kRowWarps + warp;
+      p_end = min(ps.k1 * kRowWarps, (ps.limit(p) + kSlice - 1) / kSlice);
+    }
+    p_page = p.pg.table[int64_t(ps.e) * p.pg.max_pages + ((p_slice * kSlice) >> p.pg.log2_page)];
+  };
+  auto p_issue = [&]() {
+    if (!p_more) return;
+    if (p_count == p.withhold) {
+      p_more = false;
+      return;
+    }
+    const int st = p_count % L::kStages;
+    if (lane == 0) {
+      int page = p_page;
+      if (page < 0 || page >= p.pg.n_pages) {
+        record(p.status, VARK_E_SHAPE);
+        page = 0;          // in bounds; the call's outputs are void
+      }
+      const int key0 = p_slice * kSlice;
+      const int row = ((p.pg.page_heads > 1 ? ps.h : 0) << p.pg.log2_page) + (key0 & ((1 << p.pg.log2_page) - 1));
+      const uint32_t bar = bar0 + 8u * st, dst = ring + st * L::kStage;
+      mbar_arrive_expect_tx(bar, L::kStage);
+#pragma unroll
+      for (int c = 0; c < NP; ++c) {
+        tma_load_3d(dst + c * L::kPanel, &tm_k, bar, c * 64, row, page);
+        tma_load_3d(dst + L::kHalf + c * L::kPanel, &tm_v, bar, c * 64, row, page);
+      }
+    }
+    ++p_count;
+    p_slice += kRowWarps;
+    p_settle();
+  };
+  ps.start(p, share);
+  p_settle();
+  for (int i = 0; i < L::kStages; ++i) p_issue();
+
+  // ldmatrix addresses of this lane (chunk index still to be xor-ed with the row)
+  const int lr = lane & 7, li = lane >> 3;
+  const uint32_t k_row = uint32_t(((li >> 1) * 8 + lr) * 128), k_chunk = uint32_t(li & 1);
+  const uint32_t v_row = uint32_t(((li & 1) * 8 + lr) * 128), v_chunk = uint32_t(li >> 1);
+
+  Seg cs;
+  cs.start(p, share);
+  int c_count = 0;
+  bool ok = true;
+  while (cs.next(p)) {
+    // queries of the tile, as the A operand: rows g and g + 8 of this lane
+    const RowAt ra = row_at(p, cs, g), rb = row_at(p, cs, g + 8);
+    uint32_t qa[KS][4];
+    {
+      const uint16_t* qp = p.q + (ra.token < 0 ? 0 : ra.token * p.qs[0] + ra.head * p.qs[1]) + 2 * t4;
+      const uint16_t* qb = p.q + (rb.token < 0 ? 0 : rb.token * p.qs[0] + rb.head * p.qs[1]) + 2 * t4;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        qa[k][0] = ra.token < 0 ? 0u : *reinterpret_cast<const uint32_t*>(qp + k * 16);
+        qa[k][1] = rb.token < 0 ? 0u : *reinterpret_cast<const uint32_t*>(qb + k * 16);
+        qa[k][2] = ra.token < 0 ? 0u : *reinterpret_cast<const uint32_t*>(qp + k * 16 + 8);
+        qa[k][3] = rb.token < 0 ? 0u : *reinterpret_cast<const uint32_t*>(qb + k * 16 + 8);
+      }
+    }
+    float scale[2] = {p.scale_log2, p.scale_log2};
+    if (p.tau != nullptr) {
+      if (ra.token >= 0) scale[0] *= p.tau[ra.head];
+      if (rb.token >= 0) scale[1] *= p.tau[rb.head];
+    }
+    const int lim[2] = {ra.limit, rb.limit};
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
+    const int end = min(cs.k1 * kRowWarps, (cs.limit(p) + kSlice - 1) / kSlice);
+    for (int slice = cs.k0 * kRowWarps + warp; slice < end; slice += kRowWarps) {
+      const int st = c_count % L::kStages;
+      ok = ok && mbar_wait(bar0 + 8u * st, (c_count / L::kStages) & 1, abort_flag, p.status, p.wait_limit_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      ++c_count;
+      const uint32_t sk = ring + st * L::kStage, sv = sk + L::kHalf;
+      const int key0 = slice * kSlice;
+      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint32_t b[4];
+        ldmatrix4(sk + (k >> 2) * L::kPanel + k_row + ((((k & 3) * 2 + k_chunk) ^ lr) << 4), b);
+        mma16816<DT>(s[0], qa[k], b[0], b[1]);
+        mma16816<DT>(s[1], qa[k], b[2], b[3]);
+      }
+      // scale, mask, running maximum
+      float f[2];
+      bool moved = false;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int key = key0 + n * 8 + 2 * t4 + c;
+            float& x = s[n][2 * i + c];
+            x = key < lim[i] ? x * scale[i] : -INFINITY;
+            mx = fmaxf(mx, x);
+          }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        f[i] = 1.f;
+        if (mx > m[i] + kRescale || (m[i] == -INFINITY && mx > -INFINITY)) {
+          f[i] = ex2_approx(m[i] - mx);
+          m[i] = mx;
+          moved = true;
+        }
+        const float shift = m[i] == -INFINITY ? 0.f : m[i];
+        float sum = 0.f;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float& x = s[n][2 * i + c];
+            x = ex2_approx(x - shift);
+            sum += x;
+          }
+        l[i] = l[i] * f[i] + sum;
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          o[n][0] *= f[0];
+          o[n][1] *= f[0];
+          o[n][2] *= f[1];
+          o[n][3] *= f[1];
+        }
+      }
+      // the probabilities, rounded to the values' type, are the A operand of P V
+      const uint32_t pa[4] = {pack2<DT>(s[0][0], s[0][1]), pack2<DT>(s[0][2], s[0][3]),
+                              pack2<DT>(s[1][0], s[1][1]), pack2<DT>(s[1][2], s[1][3])};
+      // rows behind the cache's end hold anything: 0 * NaN must not reach the sum
+      const int left = cs.x.len - key0;
+      const bool tail = left < kSlice;
+      const uint32_t keep0 = (2 * t4 < left ? 0xFFFFu : 0u) | (2 * t4 + 1 < left ? 0xFFFF0000u : 0u);
+      const uint32_t keep1 = (2 * t4 + 8 < left ? 0xFFFFu : 0u) | (2 * t4 + 9 < left ? 0xFFFF0000u : 0u);
+#pragma unroll
+      for (int c = 0; c < KS; ++c) {
+        uint32_t b[4];
+        ldmatrix4_trans(sv + (c >> 2) * L::kPanel + v_row + ((((c & 3) * 2 + v_chunk) ^ lr) << 4), b);
+        if (tail) {
+          b[0] &= keep0;
+          b[1] &= keep1;
+          b[2] &= keep0;
+          b[3] &= keep1;
+        }
+        mma16816<DT>(o[2 * c], pa, b[0], b[1]);
+        mma16816<DT>(o[2 * c + 1], pa, b[2], b[3]);
+      }
+      __syncwarp();        // every lane is done with the stage
+      p_issue();
+    }
+    // the 8 warps' results, relative to their own maxima
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      const int r = g + 8 * i;
+      float* mo = merge + (warp * kRowR + r) * L::kMergeStride + 2 * t4;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        *reinterpret_cast<float2*>(mo + n * 8) = make_float2(o[n][2 * i], o[n][2 * i + 1]);
+      if (t4 == 0) *reinterpret_cast<float2*>(ml + (warp * kRowR + r) * 2) = make_float2(m[i], l[i]);
+    }
+    __syncthreads();
+    {
+      const int r = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * (D / 16);
+      const RowAt a = row_at(p, cs, r);
+      if (a.token >= 0 && *abort_flag == 0) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kRowWarps; ++w) top = fmaxf(top, ml[(w * kRowR + r) * 2]);
+        const float ref = top == -INFINITY ? 0.f : top;
+        float sum = 0.f, acc[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kRowWarps; ++w) {
+          const float wgt = ex2_approx(ml[(w * kRowR + r) * 2] - ref);
+          sum = fmaf(ml[(w * kRowR + r) * 2 + 1], wgt, sum);
+          const float* mo = merge + (w * kRowR + r) * L::kMergeStride + d0;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) acc[i] = fmaf(mo[i], wgt, acc[i]);
+        }
+        const bool whole = cs.k0 == 0 && cs.k1 == cs.x.key_tiles;
+        if (whole && D == 128) {
+          store_row8<DT>(p, a, d0, acc, top, sum);
+        } else if (whole) {
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          *reinterpret_cast<uint2*>(p.out + a.token * p.os[0] + a.head * p.os[1] + d0) =
+              make_uint2(pack2<DT>(acc[0] * inv, acc[1] * inv), pack2<DT>(acc[2] * inv, acc[3] * inv));
+          if (d0 == 0 && p.lse != nullptr)
+            p.lse[int64_t(a.token) * p.Hq + a.head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        } else {
+          const int64_t slot = (int64_t(blockIdx.x) * 2 + (cs.k0 == 0 ? 1 : 0)) * kRowR + r;
+#pragma unroll
+          for (int i = 0; i < D / 16; i += 4)
+            *reinterpret_cast<float4*>(p.part_o + slot * D + d0 + i) =
+                make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+          if (d0 == 0) *reinterpret_cast<float2*>(p.part_ml + slot * 2) = make_float2(top, sum);
+        }
+      }
+    }
+    __syncthreads();
+  }
+  // Loads that nothing consumed (only after a wait that gave up) land before the CTA exits.
+  volatile int no_abort = 0;
+  for (; c_count < p_count; ++c_count)
+    mbar_wait(bar0 + 8u * (c_count % L::kStages), (c_count / L::kStages) & 1, &no_abort, nullptr);
+}
+
+// Joins the partial results of the item that starts in share c = blockIdx.x
+// and ends in a later one; blockIdx.y: 16 rows of the tile.
+template <int DT, int D, int R, int KT>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnParams p) {
+  const int c = blockIdx.x;
+  const Share s = find_share<R, KT, 256, true>(p, c);
+  // Every CTA waits, also those without an item: the launch after this one
+  // may count on the attention kernel's end.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (s.u0 == s.u1) return;
+  const Entry x = load_entry<R, KT>(p, s.e);
+  const int64_t off = s.u1 - 1 - s.base;
+  const int item = int(off / x.key_tiles);
+  const int64_t begin = s.base + int64_t(item) * x.key_tiles, end = begin + x.key_tiles;
+  if (begin < s.u0 || end <= s.u1) return;
+  Segments<R, KT> seg;
+  seg.e = s.e;
+  seg.x = x;
+  seg.h = p.pg.table_heads > 1 ? s.e % p.pg.heads : item / x.row_tiles;
+  seg.tile = item % x.row_tiles;
+  const int r = blockIdx.y * 16 + (threadIdx.x >> 4), d0 = (threadIdx.x & 15) * (D / 16);
+  const RowAt a = row_at(p, seg, r);
+  // the shares that hold a part: c, c + 1, ... while they start before the item ends
+  const int ctas = int(min(int64_t(kCtas), s.total));
+  int last = c + 1;
+  while (last + 1 < ctas && share_begin(s.total, ctas, last + 1) < end) ++last;
+  if (a.token < 0 || *reinterpret_cast<volatile int32_t*>(p.status) != 0) return;
+  auto slot = [&](int i) { return (int64_t(i) * 2 + (i == c ? 1 : 0)) * R + r; };
+  float top = -INFINITY;
+  for (int i = c; i <= last; ++i) top = fmaxf(top, p.part_ml[slot(i) * 2]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float sum = 0.f, acc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+#pragma unroll 4
+  for (int i = c; i <= last; ++i) {
+    const float2 v = *reinterpret_cast<const float2*>(p.part_ml + slot(i) * 2);
+    const float wgt = ex2_approx(v.x - ref);
+    sum = fmaf(v.y, wgt, sum);
+#pragma unroll
+    for (int d = 0; d < D / 16; d += 4) {
+      const float4 w = *reinterpret_cast<const float4*>(p.part_o + slot(i) * D + d0 + d);
+      acc[d] = fmaf(w.x, wgt, acc[d]);
+      acc[d + 1] = fmaf(w.y, wgt, acc[d + 1]);
+      acc[d + 2] = fmaf(w.z, wgt, acc[d + 2]);
+      acc[d + 3] = fmaf(w.w, wgt, acc[d + 3]);
+    }
+  }
+  if constexpr (D == 128) {
+    store_row8<DT>(p, a, d0, acc, top, sum);
+  } else {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint2*>(p.out + a.token * p.os[0] + a.head * p.os[1] + d0) =
+        make_uint2(pack2<DT>(acc[0] * inv, acc[1] * inv), pack2<DT>(acc[2] * inv, acc[3] * inv));
+    if (d0 == 0 && p.lse != nullptr)
+      p.lse[int64_t(a.token) * p.Hq + a.head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  }
+}
+
+// ------------------------------------------------------------------ host side
+static void test_hooks(AttnParams& p) {
+  p.wait_limit_ns = kWaitLimitNs;
+  p.withhold = -1;
+  if (const char* e = std::getenv("VARK_TEST_WAIT_LIMIT_MS")) {
+    const long ms = std::strtol(e, nullptr, 10);
+    if (ms > 0 && ms <= 10000) p.wait_limit_ns = uint64_t(ms) * 1000000ull;
+  }
+  if (const char* e = std::getenv("VARK_TEST_WITHHOLD_KV_TILE")) {
+    const long j = std::strtol(e, nullptr, 10);
+    if (j >= 0 && j < (1 << 20)) p.withhold = int(j);
+  }
+}
+
+static int encode_pages(CUtensorMap* m, const uint16_t* base, const Pages& pg, int D, int box_rows) {
+  const uint64_t rows = uint64_t(pg.page_heads) << pg.log2_page;
+  const uint64_t dims[3] = {uint64_t(D), rows, uint64_t(pg.n_pages)};
+  const uint64_t strides[2] = {uint64_t(D) * 2, rows * D * 2};
+  return encode_bf16_map(m, base, 3, dims, strides, uint32_t(box_rows));   // 16-bit elements, copied as they are
+}
+
+// The join starts while the attention kernel still runs (it finds its share
+// meanwhile) and waits for it before it reads a partial.
+template <typename K>
+static int launch_join(K kern, dim3 grid, const AttnParams& p, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? VARK_OK : VARK_E_CUDA;
+}
+
+template <int DT, int D>
+static int launch_rows(const CUtensorMap& k, const CUtensorMap& v, const AttnParams& p, cudaStream_t st) {
+  auto kern = rows_kernel<DT, D>;
+  const int smem = RowSmem<D>::kAlloc;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+    cudaGetLastError();
+    return VARK_E_CUDA;
+  }
+  kern<<<kCtas, kRowThreadsA, smem, st>>>(k, v, p);
+  if (cudaGetLastError() != cudaSuccess) return VARK_E_CUDA;
+  const int rc = launch_join(join_kernel<DT, D, kRowR, kRowKT>, dim3(kCtas, kRowR / 16), p, st);
+  if (rc) cudaGetLastError();
+  return rc;
+}
+
+static int64_t workspace_bytes_for(int R, int D) { return int64_t(kCtas) * 2 * R * (D + 2) * 4; }
+
+}  // namespace paged
+}  // namespace vark
+
+using namespace vark;
+using namespace vark::paged;
+
+extern "C" int64_t vark_paged_attention_workspace(int64_t n_tokens, int B, int Hq, int Hkv, int D, int page_size,
+                                                  int max_pages) {
+  if (D != 64 && D != 128) return VARK_E_SHAPE;
+  if (n_tokens < 0 || B < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || page_size < 1 || max_pages < 1)
+    return VARK_E_SHAPE;
+  return workspace_bytes_for(kRowR, D);
+}
+
+extern "C" int vark_paged_attention(int dtype, const uint16_t* q, const int64_t* q_strides, int64_t n_tokens, int B,
+                                    int Hq, int Hkv, int D, const int32_t* cu_tokens, const uint16_t* k_pages,
+                                    const uint16_t* v_pages, int64_t n_pages, int page_size,
+                                    const int32_t* page_table, int max_pages, const int32_t* cache_len,
+                                    int head_pages, const float* tau, int causal, uint16_t* out,
+                                    const int64_t* out_strides, float* lse, void* workspace, int64_t workspace_bytes,
+                                    int32_t* dev_status, void* stream) {
+  if (!q || !q_strides || !cu_tokens || !k_pages || !v_pages || !page_table || !cache_len || !out || !out_strides ||
+      !workspace || !dev_status)
+    return VARK_E_ARG;
+  if (dtype != VARK_BF16 && dtype != VARK_FP16) return VARK_E_ARG;
+  if (D != 64 && D != 128) return VARK_E_SHAPE;
+  if (n_tokens < 0 || B < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq > 65536) return VARK_E_SHAPE;
+  if (n_tokens * Hq > INT32_MAX / 2 || int64_t(B) * Hkv > (1 << 24)) return VARK_E_SHAPE;
+  AttnParams p;
+  int rc = make_pages(&p.pg, page_table, cache_len, n_pages, page_size, max_pages, Hkv, head_pages);
+  if (rc) return rc;
+  if (workspace_bytes < vark_paged_attention_workspace(n_tokens, B, Hq, Hkv, D, page_size, max_pages))
+    return VARK_E_ARG;
+  const int64_t extent[2] = {n_tokens, Hq};
+  if (!take_strides(p.qs, q_strides, extent, 2) || !take_strides(p.os, out_strides, extent, 2)) return VARK_E_ALIGN;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned16(workspace))
+    return VARK_E_ALIGN;
+  if ((rc = check_device_sm100())) return rc;
+  if (n_tokens == 0 || B == 0) return VARK_OK;
+  p.q = q; p.out = out; p.lse = lse;
+  p.cu = cu_tokens;
+  p.tau = tau;
+  p.N = n_tokens;
+  p.B = B; p.G = Hq / Hkv; p.Hq = Hq; p.causal = causal != 0;
+  p.scale_log2 = kLog2e / sqrtf(float(D));
+  p.part_ml = static_cast<float*>(workspace);
+  p.part_o = p.part_ml + int64_t(kCtas) * 2 * kRowR * 2;
+  p.status = dev_status;
+  test_hooks(p);
+  CUtensorMap tk, tv;
+  if ((rc = encode_pages(&tk, k_pages, p.pg, D, kSlice))) return rc;
+  if ((rc = encode_pages(&tv, v_pages, p.pg, D, kSlice))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == VARK_BF16)
+    return D == 128 ? launch_rows<VARK_BF16, 128>(tk, tv, p, st) : launch_rows<VARK_BF16, 64>(tk, tv, p, st);
+  return D == 128 ? launch_rows<VARK_FP16, 128>(tk, tv, p, st) : launch_rows<VARK_FP16, 64>(tk, tv, p, st);
+}

@@ -35,6 +35,7 @@ struct AttnParams {
   const float* tau;        // [Hq] or null
   int64_t N;
   int B, G, Hq, causal;
+  int split;               // 1: equal shares of the key tiles; 0: a CTA per item
   float scale_log2;        // log2(e) / sqrt(D)
   float* part_o;           // [kCtas][2][R][D]
   float* part_ml;          // [kCtas][2][R][2]
@@ -74,8 +75,13 @@ VARK_DEV Entry load_entry(const AttnParams& p, int e) {
   return x;
 }
 
+// Units of work: key tiles (split), or whole items.
+VARK_DEV int64_t entry_units(const AttnParams& p, const Entry& x) {
+  return p.split ? int64_t(x.items) * x.key_tiles : x.items;
+}
+
 struct Share {
-  int64_t total;           // units (key tiles) of the call
+  int64_t total;           // units of the call
   int64_t u0, u1;          // this CTA's units
   int e;                   // entry of the unit asked for, and its first unit
   int64_t base;
@@ -96,7 +102,7 @@ VARK_DEV Share find_share(const AttnParams& p, int cta) {
   int64_t sum = 0;
   for (int e = e0; e < e1; ++e) {
     const Entry x = load_entry<R, KT>(p, e);
-    sum += int64_t(x.items) * x.key_tiles;
+    sum += entry_units(p, x);
   }
   int64_t incl = sum;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -115,18 +121,18 @@ VARK_DEV Share find_share(const AttnParams& p, int cta) {
     if (w < warp) before += warp_sum[w];
     s.total += warp_sum[w];
   }
-  const int ctas = int(min(int64_t(kCtas), s.total));
+  const int ctas = int(p.split ? min(int64_t(kCtas), s.total) : s.total);
   s.e = 0;
   s.base = s.u0 = s.u1 = 0;
   if (cta >= ctas) return s;     // the same for every thread
-  s.u0 = share_begin(s.total, ctas, cta);
-  s.u1 = share_begin(s.total, ctas, cta + 1);
+  s.u0 = p.split ? share_begin(s.total, ctas, cta) : cta;
+  s.u1 = p.split ? share_begin(s.total, ctas, cta + 1) : cta + 1;
   const int64_t want = LAST ? s.u1 - 1 : s.u0;
   int64_t base = before + incl - sum;
   if (want >= base && want < base + sum) {
     for (int e = e0; e < e1; ++e) {
       const Entry x = load_entry<R, KT>(p, e);
-      const int64_t w = int64_t(x.items) * x.key_tiles;
+      const int64_t w = entry_units(p, x);
       if (want < base + w) {
         found_e = e;
         found_base = base;
@@ -158,17 +164,26 @@ struct Segments {
   }
   VARK_DEV bool next(const AttnParams& p) {
     if (u >= u1) return false;
-    while (u >= base + int64_t(x.items) * x.key_tiles) {
-      base += int64_t(x.items) * x.key_tiles;
+    while (u >= base + entry_units(p, x)) {
+      base += entry_units(p, x);
       x = load_entry<R, KT>(p, ++e);
     }
     const int64_t off = u - base;
-    const int item = int(off / x.key_tiles);
-    k0 = int(off - int64_t(item) * x.key_tiles);
-    k1 = int(min(int64_t(x.key_tiles), k0 + (u1 - u)));
-    u += k1 - k0;
+    int item = int(off);
+    k0 = 0;
+    k1 = x.key_tiles;
+    if (p.split) {
+      item = int(off / x.key_tiles);
+      k0 = int(off - int64_t(item) * x.key_tiles);
+      k1 = int(min(int64_t(x.key_tiles), k0 + (u1 - u)));
+      u += k1 - k0;
+    } else {
+      ++u;
+    }
     h = p.pg.table_heads > 1 ? e % p.pg.heads : item / x.row_tiles;
     tile = item % x.row_tiles;
+    // a sequence's last rows see the most keys under a causal mask: first
+    if (!p.split) tile = x.row_tiles - 1 - tile;
     return true;
   }
   // Keys that some row of the tile sees.
@@ -206,6 +221,477 @@ VARK_DEV void store_row8(const AttnParams& p, const RowAt& a, int d0, const floa
   *reinterpret_cast<uint4*>(p.out + a.token * p.os[0] + a.head * p.os[1] + d0) = w;
   if (d0 == 0 && p.lse != nullptr)
     p.lse[int64_t(a.token) * p.Hq + a.head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// ------------------------------------------------------------------ tiles kernel
+// Many rows a kv head (prompt chunks, scales): bound by the tensor cores.  A
+// CTA works on 256 rows as two tiles of 128 (A, B) that see the same key tiles,
+// so every key tile is loaded once for both.  Warp 0 loads key and value
+// tiles of 128 rows by TMA, one box per page, into one ring of slots (K_0, V_0,
+// K_1, V_1, ...); warp 1 issues the MMAs PV_A(j-1), S_A(j), PV_B(j-1), S_B(j),
+// so the softmax of one tile overlaps the products of the other; warps 4-7 and
+// 8-11 are the softmax of A and B, one thread per row (TMEM lane).  S is read
+// from tensor memory, and P written back over its first 64 columns in the type
+// of the values, where the PV MMA takes it as its A operand.  O stays in tensor
+// memory and is rescaled only when a row's maximum grows by more than 2^8.
+// The MMA warp runs its loop with all lanes and only predicates the MMAs:
+// descriptors and addresses then stay warp-uniform.
+// TMEM: S_A [0,128) S_B [128,256) O_A [256,256+D) O_B [256+D,256+2D).
+constexpr int kTileThreads = 384;
+constexpr int kTileR = 256;
+constexpr int kTileKT = 128;
+constexpr int kMaxSmem = 232448;
+
+VARK_DEV uint32_t elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+// The MMAs and commits of the thread whose `lead` is 1 (all lanes pass by).
+VARK_DEV void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+      : "memory");
+}
+VARK_DEV void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+      : "memory");
+}
+VARK_DEV void commit(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(lead)
+      : "memory");
+}
+// Instruction descriptor, kind::f16: A and B of type DT, fp32 accumulator.
+template <int DT>
+__host__ __device__ constexpr uint32_t idesc_of(int M, int N, bool b_mn_major) {
+  return (1u << 4) | (DT == VARK_BF16 ? (1u << 7) | (1u << 10) : 0u) | (uint32_t(b_mn_major) << 16) |
+         (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+
+template <int D>
+struct TileSmem {
+  static constexpr int kPanel = 128 * 128;            // 128 rows x 64 channels
+  static constexpr int kTile = (D / 64) * kPanel;
+  static constexpr int kSlots = D == 128 ? 5 : 8;
+  static constexpr int kQ = 0;                        // [2 tiles]
+  static constexpr int kRing = kQ + 2 * kTile;        // [kSlots]
+  static constexpr int kBar = kRing + kSlots * kTile;
+  static constexpr int kFull = 0, kEmpty = kSlots;    // barrier indices
+  static constexpr int kQFull = 2 * kSlots, kS = kQFull + 2, kP = kS + 2, kO = kP + 2, kDrain = kO + 2;
+  static constexpr int kNumBars = kDrain + 1;
+  static constexpr int kMisc = kBar + kNumBars * 8;   // tmem base, abort flag
+  static constexpr int kSeg = kMisc + 16;             // [8 softmax warps] segment (kept out of their registers)
+  static constexpr int kSegBytes = 96;
+  static constexpr int kAlloc = kSeg + 8 * kSegBytes + 1024;
+  static_assert(kAlloc + 1024 <= kMaxSmem, "shared memory");
+};
+
+// A place in the ring: slot i % kSlots, with the parity of its round.
+template <int SLOTS>
+struct RingAt {
+  int slot, phase;
+  VARK_DEV void skip(int n) {
+    slot += n;
+    if (slot >= SLOTS) {
+      slot -= SLOTS;
+      phase ^= 1;
+    }
+  }
+};
+
+// Key tiles of a segment that some row of the item sees.
+template <int R, int KT>
+VARK_DEV int seen_tiles(const AttnParams& p, const Segments<R, KT>& s) {
+  return max(0, min(s.k1, (s.limit(p) + KT - 1) / KT) - s.k0);
+}
+
+template <int DT, int D>
+__global__ void __launch_bounds__(kTileThreads, 1)
+tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+             const __grid_constant__ AttnParams p) {
+  using L = TileSmem<D>;
+  using Seg = Segments<kTileR, kTileKT>;
+  using Ring = RingAt<L::kSlots>;
+  constexpr int NP = D / 64;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
+  auto bar = [&](int i) { return sbase + L::kBar + 8u * uint32_t(i); };
+  auto wait = [&](int i, int phase) {
+    return mbar_wait(bar(i), uint32_t(phase), abort_flag, p.status, p.wait_limit_ns);
+  };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kSlots; ++i) {
+      mbar_init(bar(L::kFull + i), 1);
+      mbar_init(bar(L::kEmpty + i), 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(bar(L::kQFull + x), 4);
+      mbar_init(bar(L::kS + x), 1);
+      mbar_init(bar(L::kP + x), 4);
+      mbar_init(bar(L::kO + x), 1);
+    }
+    mbar_init(bar(L::kDrain), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  const Share share = find_share<kTileR, kTileKT, kTileThreads, false>(p, blockIdx.x);   // syncs the block
+  if (share.u0 == share.u1) return;
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp < 4) {
+    setmaxnreg_dec56();
+    Seg sg;
+    sg.start(p, share);
+    if (warp == 0) {
+      // -------------------------------------------------------- loader
+      const int box_log2 = min(p.pg.log2_page, 7);
+      const int boxes = kTileKT >> box_log2;          // pages a tile spans (1: a tile lies in one page)
+      Ring at = {0, 0};
+      int issued = 0;
+      bool ok = true;
+      while (ok && sg.next(p)) {
+        const int nt = seen_tiles(p, sg);
+        const int32_t* table = p.pg.table + int64_t(sg.e) * p.pg.max_pages;
+        auto page_at = [&](int j) {                   // page of this lane's box of tile j
+          const int key = (sg.k0 + j) * kTileKT + (lane << box_log2);
+          return lane < boxes && key < sg.x.len ? table[key >> p.pg.log2_page] : 0;
+        };
+        int page = nt > 0 ? page_at(0) : 0;
+        for (int j = 0; ok && j < nt; ++j) {
+          const int next_page = j + 1 < nt ? page_at(j + 1) : 0;
+          if (page < 0 || page >= p.pg.n_pages) {
+            record(p.status, VARK_E_SHAPE);
+            page = 0;           // in bounds; the call's outputs are void
+          }
+          const int key0 = (sg.k0 + j) * kTileKT;
+          const int used = min(boxes, (min(kTileKT, sg.x.len - key0) + (1 << box_log2) - 1) >> box_log2);
+          const int row = ((p.pg.page_heads > 1 ? sg.h : 0) << p.pg.log2_page) +
+                          ((key0 + (lane << box_log2)) & ((1 << p.pg.log2_page) - 1));
+          const uint32_t bytes = uint32_t(used) << (box_log2 + (D == 128 ? 8 : 7));
+#pragma unroll
+          for (int which = 0; which < 2; ++which) {
+            if (issued / 2 == p.withhold) ok = false;   // test hook: this tile never arrives
+            ok = ok && (issued < L::kSlots || wait(L::kEmpty + at.slot, at.phase ^ 1));
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const uint32_t full = bar(L::kFull + at.slot);
+            const uint32_t dst = sbase + L::kRing + at.slot * L::kTile + (lane << (box_log2 + 7));
+            if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+            __syncwarp();
+            if (lane < used) {
+#pragma unroll
+              for (int c = 0; c < NP; ++c)
+                tma_load_3d(dst + c * L::kPanel, which ? &tm_v : &tm_k, full, c * 64, row, page);
+            }
+            ++issued;
+            at.skip(1);
+          }
+          page = next_page;
+        }
+      }
+      // Every load has landed before the CTA exits (at once unless a wait gave up).
+      volatile int no_abort = 0;
+      const int back = min(issued, L::kSlots);
+      for (int i = 0; i < back; ++i) {
+        const int k = issued - 1 - i;
+        mbar_wait(bar(L::kFull + k % L::kSlots), (k / L::kSlots) & 1, &no_abort, nullptr);
+      }
+    } else if (warp == 1) {
+      // -------------------------------------------------------- MMA issue
+      const uint32_t lead = elect_one();
+      constexpr uint32_t idesc_s = idesc_of<DT>(128, 128, false);
+      constexpr uint32_t idesc_o = idesc_of<DT>(128, D, true);
+      const uint64_t dq = smem_desc_sw128(sbase + L::kQ, 16, 1024);
+      const uint64_t dk = smem_desc_sw128(sbase + L::kRing, 16, 1024);
+      const uint64_t dv = smem_desc_sw128(sbase + L::kRing, L::kPanel, 1024);
+      auto issue_s = [&](int x, int slot) {
+        const uint64_t a = dq + uint32_t(x * (L::kTile >> 4)), b = dk + uint32_t(slot * (L::kTile >> 4));
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = ((k >> 2) * L::kPanel + (k & 3) * 32) >> 4;
+          mma_ss(lead, tmem + x * 128, a + off, b + off, idesc_s, k > 0);
+        }
+      };
+      auto issue_pv = [&](int x, int slot, uint32_t acc) {
+        const uint64_t b = dv + uint32_t(slot * (L::kTile >> 4));
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_ts(lead, tmem + 256 + x * D, tmem + x * 128 + k * 8, b + k * (2048 >> 4), idesc_o, k > 0 ? 1u : acc);
+      };
+      Ring kr = {0, 0}, vr = {1, 0};
+      int q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+      bool ok = true;
+      while (ok && sg.next(p)) {
+        const int nt = seen_tiles(p, sg);
+        const int n_act = sg.x.n * p.G - sg.tile * kTileR > 128 ? 2 : 1;
+        for (int j = 0; ok && j <= nt && nt > 0; ++j) {
+          if (j < nt) ok = wait(L::kFull + kr.slot, kr.phase);
+          if (ok && j > 0) ok = wait(L::kFull + vr.slot, vr.phase);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (x >= n_act || !ok) break;
+            if (j > 0) {
+              ok = wait(L::kP + x, p_phase[x]);
+              if (!ok) break;
+              p_phase[x] ^= 1;
+              tc_fence_after();
+              issue_pv(x, vr.slot, j > 1);
+            } else {
+              ok = wait(L::kQFull + x, q_phase[x]);
+              if (!ok) break;
+              q_phase[x] ^= 1;
+              tc_fence_after();
+            }
+            if (j < nt) {
+              issue_s(x, kr.slot);
+              commit(lead, bar(L::kS + x));
+            } else {
+              commit(lead, bar(L::kO + x));
+            }
+          }
+          if (!ok) break;
+          if (j > 0) {
+            commit(lead, bar(L::kEmpty + vr.slot));
+            vr.skip(2);
+          }
+          if (j < nt) {
+            commit(lead, bar(L::kEmpty + kr.slot));
+            kr.skip(2);
+          }
+        }
+      }
+      // All MMAs are done before tensor memory is released.
+      commit(lead, bar(L::kDrain));
+      volatile int no_abort = 0;
+      mbar_wait(bar(L::kDrain), 0, &no_abort, nullptr);
+    }
+  } else {
+    setmaxnreg_inc224();
+    // ---------------------------------------------------------- softmax
+    const int x = (warp >> 2) - 1;
+    const int r = threadIdx.x - 128 * (x + 1);          // row within the tile = TMEM lane
+    const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + x * 128 + lane_base;
+    const uint32_t tO = tmem + 256 + x * D + lane_base;
+    int s_phase = 0, o_phase = 0;
+    Ring vr = {1, 0};
+    bool ok = true;
+    static_assert(sizeof(Seg) <= L::kSegBytes, "segment");
+    Seg& sg = *reinterpret_cast<Seg*>(smem + L::kSeg + (warp - 4) * L::kSegBytes);
+    auto next_segment = [&]() {
+      __syncwarp();
+      const int more = __any_sync(0xffffffffu, lane == 0 && sg.next(p));
+      __syncwarp();
+      return more != 0;
+    };
+    if (lane == 0) sg.start(p, share);
+    while (ok && next_segment()) {
+      const int nt = seen_tiles(p, sg);
+      const bool active = x == 0 || sg.x.n * p.G - sg.tile * kTileR > 128;
+      if (!active) continue;      // (only tile B can be empty)
+      const RowAt row = row_at(p, sg, x * 128 + r);
+      float qk2 = p.scale_log2;
+      if (p.tau != nullptr && row.token >= 0) qk2 *= p.tau[row.head];
+      // Q to shared memory, 128-byte swizzled.  S_X of the last segment is
+      // complete, so its Q is free.  Under a negative temperature the query's
+      // sign is turned instead, so the largest score gives the largest logit.
+      if (nt > 0) {
+        const uint32_t flip = qk2 < 0.f ? 0x80008000u : 0u;
+        qk2 = fabsf(qk2);
+        const uint16_t* src = row.token < 0 ? nullptr : p.q + row.token * p.qs[0] + row.head * p.qs[1];
+        const uint32_t dst = sbase + L::kQ + x * L::kTile + r * 128;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          uint4 w = make_uint4(0u, 0u, 0u, 0u);
+          if (src != nullptr) w = *reinterpret_cast<const uint4*>(src + c * 8);
+          w.x ^= flip; w.y ^= flip; w.z ^= flip; w.w ^= flip;
+          st_shared_v4(dst + (c >> 3) * L::kPanel + (((c & 7) ^ (r & 7)) << 4), w);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kQFull + x));
+      }
+      float m_used = -INFINITY, l_sum = 0.f;
+      int seen = row.limit - sg.k0 * kTileKT;           // columns of the tile that this row sees,
+      int held = sg.x.len - sg.k0 * kTileKT;            // and that the cache holds
+      for (int j = 0; j < nt; ++j) {
+        ok = __all_sync(0xffffffffu, wait(L::kS + x, s_phase));
+        if (!ok) break;
+        s_phase ^= 1;
+        tc_fence_after();
+        float sv[128];
+        {
+          uint32_t v[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, v[c]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            reg_fence32(v[c]);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sv[c * 32 + i] = __uint_as_float(v[c][i]);
+          }
+        }
+        const bool edge = __any_sync(0xffffffffu, seen < kTileKT);
+        if (edge) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c) sv[c] = c < seen ? sv[c] * qk2 : -INFINITY;
+        }
+        float m0 = sv[0], m1 = sv[1], m2 = sv[2], m3 = sv[3];
+#pragma unroll
+        for (int c = 4; c < 124; c += 8) {
+          m0 = fmax3(m0, sv[c + 0], sv[c + 1]);
+          m1 = fmax3(m1, sv[c + 2], sv[c + 3]);
+          m2 = fmax3(m2, sv[c + 4], sv[c + 5]);
+          m3 = fmax3(m3, sv[c + 6], sv[c + 7]);
+        }
+        m0 = fmax3(m0, sv[124], sv[125]);
+        m1 = fmax3(m1, sv[126], sv[127]);
+        const float mul = edge ? 1.f : qk2;
+        const float m_tile = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * mul;
+        float f = 1.f;
+        if (m_tile > m_used + kRescale || (m_used == -INFINITY && m_tile > -INFINITY)) {
+          f = ex2_approx(m_used - m_tile);
+          m_used = m_tile;
+          l_sum *= f;
+        }
+        if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {   // O_X is stable: S_X(j) came after PV_X(j-1)
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32];
+            tmem_ld32(tO + c * 32, v);
+            tmem_wait_ld();
+            reg_fence32(v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+            tmem_st32(tO + c * 32, v);
+          }
+        }
+        const float shift = m_used == -INFINITY ? 0.f : -m_used;
+#pragma unroll
+        for (int c = 0; c < 128; c += 2) ffma2(sv[c], sv[c + 1], sv[c], sv[c + 1], mul, mul, shift, shift);
+#pragma unroll
+        for (int c = 0; c < 128; ++c) sv[c] = ex2_approx(sv[c]);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) pk[c] = pack2<DT>(sv[64 * q + 2 * c], sv[64 * q + 2 * c + 1]);
+          tmem_st32(tS + q * 32, pk);
+        }
+        // The values' rows behind the cache's end hold anything, and 0 * NaN
+        // must not reach O: tile A's threads clear them (PV_B comes after
+        // PV_A, which waits for these threads).
+        if (x == 0 && held < kTileKT) {
+          ok = __all_sync(0xffffffffu, wait(L::kFull + vr.slot, vr.phase));
+          if (!ok) break;
+          if (r >= held) {
+            const uint32_t dst = sbase + L::kRing + vr.slot * L::kTile + r * 128;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+              st_shared_v4(dst + (c >> 3) * L::kPanel + ((c & 7) << 4), make_uint4(0u, 0u, 0u, 0u));
+          }
+          fence_proxy_async_smem();
+        }
+        vr.skip(2);
+        seen -= kTileKT;
+        held -= kTileKT;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kP + x));
+        float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f, a4 = 0.f, a5 = 0.f, a6 = 0.f, a7 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 128; c += 8) {
+          fadd2(a0, a1, a0, a1, sv[c + 0], sv[c + 1]);
+          fadd2(a2, a3, a2, a3, sv[c + 2], sv[c + 3]);
+          fadd2(a4, a5, a4, a5, sv[c + 4], sv[c + 5]);
+          fadd2(a6, a7, a6, a7, sv[c + 6], sv[c + 7]);
+        }
+        l_sum += ((a0 + a1) + (a2 + a3)) + ((a4 + a5) + (a6 + a7));
+      }
+      if (!ok) break;
+      if (nt > 0) {
+        ok = __all_sync(0xffffffffu, wait(L::kO + x, o_phase));
+        if (!ok) break;
+        o_phase ^= 1;
+        tc_fence_after();
+      }
+      const bool whole = sg.k0 == 0 && sg.k1 == sg.x.key_tiles;
+      const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;      // no key: zeros
+      const int64_t slot = (int64_t(blockIdx.x) * 2 + (sg.k0 == 0 ? 1 : 0)) * kTileR + x * 128 + r;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t v[32];
+        if (nt > 0) {
+          tmem_ld32(tO + c * 32, v);
+          tmem_wait_ld();
+          reg_fence32(v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0u;
+        }
+        if (row.token < 0) continue;
+        if (whole) {
+          uint16_t* o = p.out + row.token * p.os[0] + row.head * p.os[1] + c * 32;
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            uint4 w;
+            w.x = pack2<DT>(__uint_as_float(v[i + 0]) * inv, __uint_as_float(v[i + 1]) * inv);
+            w.y = pack2<DT>(__uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv);
+            w.z = pack2<DT>(__uint_as_float(v[i + 4]) * inv, __uint_as_float(v[i + 5]) * inv);
+            w.w = pack2<DT>(__uint_as_float(v[i + 6]) * inv, __uint_as_float(v[i + 7]) * inv);
+            *reinterpret_cast<uint4*>(o + i) = w;
+          }
+        } else {
+          float* o = p.part_o + slot * D + c * 32;
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<uint4*>(o + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        }
+      }
+      if (row.token >= 0) {
+        if (!whole)
+          *reinterpret_cast<float2*>(p.part_ml + slot * 2) = make_float2(m_used, l_sum);
+        else if (p.lse != nullptr)
+          p.lse[int64_t(row.token) * p.Hq + row.head] =
+              l_sum == 0.f ? -INFINITY : (m_used + log2f(l_sum)) * kLn2;
+      }
+      tc_fence_before();        // O has been read: the next segment's first PV, after kP, may write it
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc(tmem, 512);
+  }
 }
 
 // ------------------------------------------------------------------ rows kernel
@@ -576,6 +1062,9 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
 }
 
 // ------------------------------------------------------------------ host side
+constexpr int kTileRows = 32;      // mean rows a (sequence, kv head) above which the tiles kernel runs
+constexpr int kWaves = 4;          // items for this many rounds of the device: no split along the keys
+
 static void test_hooks(AttnParams& p) {
   p.wait_limit_ns = kWaitLimitNs;
   p.withhold = -1;
@@ -613,6 +1102,23 @@ static int launch_join(K kern, dim3 grid, const AttnParams& p, cudaStream_t st) 
 }
 
 template <int DT, int D>
+static int launch_tiles(const CUtensorMap& k, const CUtensorMap& v, const AttnParams& p, int64_t grid,
+                        cudaStream_t st) {
+  auto kern = tiles_kernel<DT, D>;
+  const int smem = TileSmem<D>::kAlloc;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+    cudaGetLastError();
+    return VARK_E_CUDA;
+  }
+  kern<<<unsigned(grid), kTileThreads, smem, st>>>(k, v, p);
+  if (cudaGetLastError() != cudaSuccess) return VARK_E_CUDA;
+  if (!p.split) return VARK_OK;
+  const int rc = launch_join(join_kernel<DT, D, kTileR, kTileKT>, dim3(kCtas, kTileR / 16), p, st);
+  if (rc) cudaGetLastError();
+  return rc;
+}
+
+template <int DT, int D>
 static int launch_rows(const CUtensorMap& k, const CUtensorMap& v, const AttnParams& p, cudaStream_t st) {
   auto kern = rows_kernel<DT, D>;
   const int smem = RowSmem<D>::kAlloc;
@@ -627,7 +1133,26 @@ static int launch_rows(const CUtensorMap& k, const CUtensorMap& v, const AttnPar
   return rc;
 }
 
-static int64_t workspace_bytes_for(int R, int D) { return int64_t(kCtas) * 2 * R * (D + 2) * 4; }
+// How a call is run, from its shapes alone (the lengths are on the device).
+struct Variant {
+  bool tiles;              // tensor-core tiles of 256 rows, or rows of 16
+  bool split;
+  int64_t items;           // at most this many items
+};
+static Variant choose(int64_t n_tokens, int B, int Hq, int Hkv) {
+  const int64_t G = Hq / Hkv;
+  Variant v;
+  const int64_t rows = n_tokens * G;                  // of a kv head, over all sequences
+  v.tiles = rows > int64_t(B) * kTileRows;
+  v.items = (rows / kTileR + B) * Hkv;
+  v.split = !v.tiles || rows / kTileR * Hkv < int64_t(kWaves) * kCtas;
+  return v;
+}
+
+static int64_t workspace_bytes_for(const Variant& v, int D) {
+  if (!v.split) return 16;
+  return int64_t(kCtas) * 2 * (v.tiles ? kTileR : kRowR) * (D + 2) * 4;
+}
 
 }  // namespace paged
 }  // namespace vark
@@ -640,7 +1165,7 @@ extern "C" int64_t vark_paged_attention_workspace(int64_t n_tokens, int B, int H
   if (D != 64 && D != 128) return VARK_E_SHAPE;
   if (n_tokens < 0 || B < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || page_size < 1 || max_pages < 1)
     return VARK_E_SHAPE;
-  return workspace_bytes_for(kRowR, D);
+  return workspace_bytes_for(choose(n_tokens, B, Hq, Hkv), D);
 }
 
 extern "C" int vark_paged_attention(int dtype, const uint16_t* q, const int64_t* q_strides, int64_t n_tokens, int B,
@@ -674,14 +1199,26 @@ extern "C" int vark_paged_attention(int dtype, const uint16_t* q, const int64_t*
   p.N = n_tokens;
   p.B = B; p.G = Hq / Hkv; p.Hq = Hq; p.causal = causal != 0;
   p.scale_log2 = kLog2e / sqrtf(float(D));
+  const Variant var = choose(n_tokens, B, Hq, Hkv);
+  if (var.items > INT32_MAX) return VARK_E_SHAPE;
+  p.split = var.split;
   p.part_ml = static_cast<float*>(workspace);
-  p.part_o = p.part_ml + int64_t(kCtas) * 2 * kRowR * 2;
+  p.part_o = p.part_ml + int64_t(kCtas) * 2 * (var.tiles ? kTileR : kRowR) * 2;
   p.status = dev_status;
   test_hooks(p);
+  const int box = var.tiles ? (page_size < kTileKT ? page_size : kTileKT) : kSlice;
   CUtensorMap tk, tv;
-  if ((rc = encode_pages(&tk, k_pages, p.pg, D, kSlice))) return rc;
-  if ((rc = encode_pages(&tv, v_pages, p.pg, D, kSlice))) return rc;
+  if ((rc = encode_pages(&tk, k_pages, p.pg, D, box))) return rc;
+  if ((rc = encode_pages(&tv, v_pages, p.pg, D, box))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (var.tiles) {
+    const int64_t grid = var.split ? kCtas : var.items;
+    if (dtype == VARK_BF16)
+      return D == 128 ? launch_tiles<VARK_BF16, 128>(tk, tv, p, grid, st)
+                      : launch_tiles<VARK_BF16, 64>(tk, tv, p, grid, st);
+    return D == 128 ? launch_tiles<VARK_FP16, 128>(tk, tv, p, grid, st)
+                    : launch_tiles<VARK_FP16, 64>(tk, tv, p, grid, st);
+  }
   if (dtype == VARK_BF16)
     return D == 128 ? launch_rows<VARK_BF16, 128>(tk, tv, p, st) : launch_rows<VARK_BF16, 64>(tk, tv, p, st);
   return D == 128 ? launch_rows<VARK_FP16, 128>(tk, tv, p, st) : launch_rows<VARK_FP16, 64>(tk, tv, p, st);

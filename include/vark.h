@@ -549,7 +549,7 @@ int vark_pruned_attention_int3(const uint16_t* q, const uint8_t* kq, const uint8
  * Chunk: the new tokens of all sequences one behind another; cu_tokens (dev
  *   int32 [B + 1], ascending from 0) gives their bounds, sequence b holding
  *   tokens cu_tokens[b] .. cu_tokens[b + 1] - 1, possibly none.  Tokens from
- *   cu_tokens[B] on are padding: not read, and their outputs not written.
+ *   cu_tokens[B] on are padding: their outputs are not written.
  * Pool: k_pages, v_pages dev [n_pages][H][page_size][D], page_size 16, 32, 64,
  *   128 or 256.  With head_pages = 1 a page holds rows of a single head,
  *   [n_pages][page_size][D], and every (sequence, head) has its own list and
@@ -592,7 +592,7 @@ enum vark_norm {
  *                output and weight).
  *   q_out, k_out dev, by their own strides; may be q, k themselves (same
  *                strides), else they must not overlap the inputs.
- *   B, T         >= 0;  Hq, Hk >= 1;  D 64 or 128.
+ *   B, T         >= 0, B * T < 2^31 - 128;  Hq, Hk >= 1, <= 65536;  D 64 or 128.
  *   norm         vark_norm;  eps >= 0.
  *   q_weight, k_weight  dev fp32 [D], or NULL for ones.
  *   rope         dev fp32 [rope_len][2][rope_dim / 2]: a position's cosines,

@@ -8,18 +8,18 @@
 // * w, L2 y = x / max(sqrt(sum(x^2)), eps) * w; a pair (a, b) of the rotated
 // channels becomes (a cos - b sin, a sin + b cos).  One rounding, at the store.
 //
-// Layout: D / 8 lanes hold a row, 8 channels (one 16-byte vector) each, so the
-// sum of squares takes log2(D / 8) shuffles and the other half of a
-// half-split pair is one lane's vector away.  A warp takes one token and up to
-// 8 heads of it: all rows are loaded first, and the token's cosines and sines
-// are read once for all of them.
+// Layout: D / 16 lanes hold a row, two vectors of 8 channels each.  The two are
+// the halves of the lane's 8 rotated pairs (half-split pairs are R / 2 apart),
+// so the rotation needs no exchange between lanes and the sum of squares
+// log2(D / 16) shuffles.  A warp takes one token and up to 16 heads of it: all
+// rows are loaded first, and the token's cosines and sines are read once for
+// all of them.
 #include "vark_paged.cuh"
 
 namespace vark {
 namespace paged {
 
 constexpr int kRowThreads = 128;
-constexpr int kHeadsPerWarp = 8;
 
 struct Rotation {
   const float* table;       // [rope_len][2][dim / 2], or null
@@ -27,84 +27,91 @@ struct Rotation {
   int len, dim, pairs;
 };
 
-// One lane's share of a token's rotation: which of its 8 channels turn, and
-// the cosines and sines they need.
-template <int LANES>
-struct LaneRotation {
-  float c[8], s[8];      // halves: 8 pairs; pairs: the first 4
-  int partner;           // halves: lane (within the row) that holds the other half
-  bool turns, first;     // first: this lane holds the a-half
+// A lane's two vectors of a row (v: their indices) and what turns them.
+template <int D>
+struct Lane {
+  int v[2];
+  bool turns;              // else both pass through
+  float c[8], s[8];        // of pair e; adjacent pairs: 0-3 of the first vector, 4-7 of the second
 
-  VARK_DEV void load(const Rotation& r, int pos, int li) {
-    turns = r.table != nullptr && li * 8 < r.dim;
-    first = true;
-    partner = li;
+  VARK_DEV void place(const Rotation& r, int li) {
+    const int half = r.table != nullptr ? r.dim >> 4 : 0;      // vectors in half the rotated channels
+    turns = li < half;
+    v[0] = turns ? li : 2 * li;
+    v[1] = turns ? li + half : 2 * li + 1;
+  }
+  VARK_DEV void load(const Rotation& r, int pos) {
     if (!turns) return;
-    const int half = r.dim >> 1;
     const float* row = r.table + int64_t(pos) * r.dim;
-    if (r.pairs) {
-      const float4 cc = *reinterpret_cast<const float4*>(row + li * 4);
-      const float4 ss = *reinterpret_cast<const float4*>(row + half + li * 4);
-      c[0] = cc.x; c[1] = cc.y; c[2] = cc.z; c[3] = cc.w;
-      s[0] = ss.x; s[1] = ss.y; s[2] = ss.z; s[3] = ss.w;
-    } else {
-      first = li * 8 < half;
-      partner = first ? li + (half >> 3) : li - (half >> 3);
-      const int j = first ? li * 8 : li * 8 - half;
+    const int half = r.dim >> 1;
 #pragma unroll
-      for (int e = 0; e < 8; e += 4) {
-        const float4 cc = *reinterpret_cast<const float4*>(row + j + e);
-        const float4 ss = *reinterpret_cast<const float4*>(row + half + j + e);
-        c[e] = cc.x; c[e + 1] = cc.y; c[e + 2] = cc.z; c[e + 3] = cc.w;
-        s[e] = ss.x; s[e + 1] = ss.y; s[e + 2] = ss.z; s[e + 3] = ss.w;
-      }
+    for (int e = 0; e < 2; ++e) {
+      const int j = r.pairs ? v[e] * 4 : v[0] * 8 + e * 4;
+      const float4 cc = *reinterpret_cast<const float4*>(row + j);
+      const float4 ss = *reinterpret_cast<const float4*>(row + half + j);
+      c[4 * e] = cc.x; c[4 * e + 1] = cc.y; c[4 * e + 2] = cc.z; c[4 * e + 3] = cc.w;
+      s[4 * e] = ss.x; s[4 * e + 1] = ss.y; s[4 * e + 2] = ss.z; s[4 * e + 3] = ss.w;
     }
   }
 };
 
-// Norm and rotation of one row held by LANES lanes (every lane of the warp
-// calls it; lanes without a row pass zeros).
-template <int DT, int LANES>
-VARK_DEV uint4 norm_rotate(uint4 w, int norm, float eps, bool weighted, const float (&wt)[8], const Rotation& rot,
-                           const LaneRotation<LANES>& lr) {
-  float x[8];
+template <int DT>
+VARK_DEV void unpack8(const uint4& w, float* x) {
   unpack2<DT>(w.x, x[0], x[1]);
   unpack2<DT>(w.y, x[2], x[3]);
   unpack2<DT>(w.z, x[4], x[5]);
   unpack2<DT>(w.w, x[6], x[7]);
+}
+template <int DT>
+VARK_DEV uint4 pack8(const float* x) {
+  return make_uint4(pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]), pack2<DT>(x[6], x[7]));
+}
+
+// Norm and rotation of one row, in place (every lane of the warp calls it;
+// lanes without a row pass zeros).
+template <int DT, int D>
+VARK_DEV void norm_rotate(uint4 (&w)[2], int norm, float eps, bool weighted, const float (&wt)[16], const Rotation& rot,
+                          const Lane<D>& ln) {
+  float x[16];
+  unpack8<DT>(w[0], x);
+  unpack8<DT>(w[1], x + 8);
   if (norm != VARK_NORM_NONE) {
-    float ss = 0.f;
+    float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+    for (int e = 0; e < 8; ++e) {
+      s0 = fmaf(x[e], x[e], s0);
+      s1 = fmaf(x[8 + e], x[8 + e], s1);
+    }
+    float ss = s0 + s1;
 #pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float inv = norm == VARK_NORM_RMS ? 1.f / sqrtf(ss * (1.f / (8 * LANES)) + eps) : 1.f / fmaxf(sqrtf(ss), eps);
+    for (int o = D / 32; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float inv = norm == VARK_NORM_RMS ? 1.f / sqrtf(ss * (1.f / D) + eps) : 1.f / fmaxf(sqrtf(ss), eps);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] *= inv;
+    for (int e = 0; e < 16; ++e) x[e] *= inv;
   }
   if (weighted) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] *= wt[e];
+    for (int e = 0; e < 16; ++e) x[e] *= wt[e];
   }
-  if (rot.table != nullptr) {
+  if (ln.turns) {
     if (rot.pairs) {
-      if (lr.turns) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float a = x[2 * e], b = x[2 * e + 1];
-          x[2 * e] = a * lr.c[e] - b * lr.s[e];
-          x[2 * e + 1] = a * lr.s[e] + b * lr.c[e];
-        }
+      for (int e = 0; e < 8; ++e) {
+        const float a = x[2 * e], b = x[2 * e + 1];
+        x[2 * e] = a * ln.c[e] - b * ln.s[e];
+        x[2 * e + 1] = a * ln.s[e] + b * ln.c[e];
       }
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float o = __shfl_sync(0xffffffffu, x[e], lr.partner, LANES);
-        if (lr.turns) x[e] = lr.first ? x[e] * lr.c[e] - o * lr.s[e] : o * lr.s[e] + x[e] * lr.c[e];
+        const float a = x[e], b = x[8 + e];
+        x[e] = a * ln.c[e] - b * ln.s[e];
+        x[8 + e] = a * ln.s[e] + b * ln.c[e];
       }
     }
   }
-  return make_uint4(pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]), pack2<DT>(x[6], x[7]));
+  w[0] = pack8<DT>(x);
+  w[1] = pack8<DT>(x + 8);
 }
 
 // -1: the token is padding (not written); -2: position outside the table.
@@ -114,12 +121,13 @@ VARK_DEV int token_position(const Rotation& r, int64_t token) {
   return p < 0 ? -1 : (p >= r.len ? -2 : p);
 }
 
-VARK_DEV void load_weight(const float* w, int li, float (&wt)[8]) {
+VARK_DEV void load_weight(const float* w, const int (&v)[2], float (&wt)[16]) {
   if (w == nullptr) return;
-  const float4 a = *reinterpret_cast<const float4*>(w + li * 8);
-  const float4 b = *reinterpret_cast<const float4*>(w + li * 8 + 4);
-  wt[0] = a.x; wt[1] = a.y; wt[2] = a.z; wt[3] = a.w;
-  wt[4] = b.x; wt[5] = b.y; wt[6] = b.z; wt[7] = b.w;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float4 a = *reinterpret_cast<const float4*>(w + v[e >> 1] * 8 + (e & 1) * 4);
+    wt[4 * e] = a.x; wt[4 * e + 1] = a.y; wt[4 * e + 2] = a.z; wt[4 * e + 3] = a.w;
+  }
 }
 
 struct RowTensor {
@@ -132,51 +140,56 @@ struct RowTensor {
 
 struct NormRopeParams {
   RowTensor t[2];          // queries, keys
-  int T;
-  int64_t tokens;          // B * T
-  int blocks[2];           // warps a token takes for the queries' heads, the keys'
+  int T, tokens;           // tokens = B * T
+  int q_blocks;            // grid rows of the queries' heads; the keys' follow
   int norm;
   float eps;
   Rotation rot;
   int32_t* status;
 };
 
+constexpr int kQkHeads = 16;       // heads of a warp's token
+
 template <int DT, int D>
 __global__ void __launch_bounds__(kRowThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kIters = kHeadsPerWarp / kRows;
-  const int lane = threadIdx.x & 31, li = lane % kLanes, sub = lane / kLanes;
-  const int per_token = p.blocks[0] + p.blocks[1];
-  const int64_t unit = int64_t(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
-  const int64_t token = unit / per_token;
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes, kIters = kQkHeads / kRows;
+  const int lane = threadIdx.x & 31, li = lane % kLanes;
+  const int token = int(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
   if (token >= p.tokens) return;
-  int blk = int(unit - token * per_token);
-  const int which = blk >= p.blocks[0];
-  if (which) blk -= p.blocks[0];
-  const RowTensor& t = p.t[which];
+  const bool keys = int(blockIdx.y) >= p.q_blocks;
+  const RowTensor& t = p.t[keys];
+  const int h0 = (int(blockIdx.y) - (keys ? p.q_blocks : 0)) * kQkHeads + lane / kLanes;
+  const int b = token / p.T, i = token - b * p.T;
+  const uint16_t* src = t.src + b * t.ss[0] + i * t.ss[1];
+  uint16_t* dst = t.dst + b * t.ds[0] + i * t.ds[1];
+  Lane<D> ln;
+  ln.place(p.rot, li);
+  uint4 w[kIters][2];
+#pragma unroll
+  for (int r = 0; r < kIters; ++r) {
+    const int h = h0 + r * kRows;
+    w[r][0] = w[r][1] = make_uint4(0u, 0u, 0u, 0u);
+    if (h < t.heads) {
+      w[r][0] = ld_stream(src + h * t.ss[2] + ln.v[0] * 8);
+      w[r][1] = ld_stream(src + h * t.ss[2] + ln.v[1] * 8);
+    }
+  }
   const int pos = token_position(p.rot, token);
   if (pos < 0) {
     if (pos == -2 && lane == 0) record(p.status, VARK_E_SHAPE);
     return;
   }
-  const int64_t b = token / p.T, i = token - b * p.T;
-  const uint16_t* src = t.src + b * t.ss[0] + i * t.ss[1] + li * 8;
-  uint16_t* dst = t.dst + b * t.ds[0] + i * t.ds[1] + li * 8;
-  const int h0 = blk * kHeadsPerWarp + sub;
-  uint4 v[kIters];
+  ln.load(p.rot, pos);
+  float wt[16];
+  load_weight(t.weight, ln.v, wt);
 #pragma unroll
   for (int r = 0; r < kIters; ++r) {
     const int h = h0 + r * kRows;
-    v[r] = h < t.heads ? ld_stream(src + h * t.ss[2]) : make_uint4(0u, 0u, 0u, 0u);
-  }
-  LaneRotation<kLanes> lr;
-  lr.load(p.rot, pos, li);
-  float wt[8];
-  load_weight(t.weight, li, wt);
-#pragma unroll
-  for (int r = 0; r < kIters; ++r) {
-    const int h = h0 + r * kRows;
-    const uint4 o = norm_rotate<DT, kLanes>(v[r], p.norm, p.eps, t.weight != nullptr, wt, p.rot, lr);
-    if (h < t.heads) *reinterpret_cast<uint4*>(dst + h * t.ds[2]) = o;
+    norm_rotate<DT, D>(w[r], p.norm, p.eps, t.weight != nullptr, wt, p.rot, ln);
+    if (h < t.heads) {
+      *reinterpret_cast<uint4*>(dst + h * t.ds[2] + ln.v[0] * 8) = w[r][0];
+      *reinterpret_cast<uint4*>(dst + h * t.ds[2] + ln.v[1] * 8) = w[r][1];
+    }
   }
 }
 
@@ -188,9 +201,7 @@ struct AppendParams {
   uint16_t* v_pages;
   Pages pg;
   const int32_t* cu;       // [B + 1]
-  int B;
-  int64_t tokens;
-  int blocks;              // warps a token takes
+  int B, tokens;
   const float* weight;
   int norm;
   float eps;
@@ -214,14 +225,33 @@ VARK_DEV int find_sequence(const int32_t* cu, int B, int64_t token, int lane) {
   }
 }
 
+constexpr int kKvHeads = 8;        // heads of a warp's token
+
 template <int DT, int D>
 __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_constant__ AppendParams p) {
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kIters = kHeadsPerWarp / kRows;
-  const int lane = threadIdx.x & 31, li = lane % kLanes, sub = lane / kLanes;
-  const int64_t unit = int64_t(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
-  const int64_t token = unit / p.blocks;
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes, kIters = (kKvHeads + kRows - 1) / kRows;
+  const int lane = threadIdx.x & 31, li = lane % kLanes;
+  const int token = int(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
   if (token >= p.tokens) return;
-  const int h0 = int(unit - token * p.blocks) * kHeadsPerWarp + sub;
+  const int h0 = int(blockIdx.y) * kKvHeads + lane / kLanes;
+  Lane<D> ln;
+  ln.place(p.rot, li);
+  // The rows are asked for before the search: it takes a few dependent loads.
+  const uint16_t* ks = p.k + token * p.ks[0];
+  const uint16_t* vs = p.v + token * p.vs[0];
+  uint4 kw[kIters][2], vw[kIters][2];
+#pragma unroll
+  for (int r = 0; r < kIters; ++r) {
+    const int h = h0 + r * kRows;
+    kw[r][0] = kw[r][1] = vw[r][0] = vw[r][1] = make_uint4(0u, 0u, 0u, 0u);
+    if (h < p.pg.heads) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        kw[r][e] = ld_stream(ks + h * p.ks[1] + ln.v[e] * 8);
+        vw[r][e] = ld_stream(vs + h * p.vs[1] + ln.v[e] * 8);
+      }
+    }
+  }
   const int pos = token_position(p.rot, token);
   const int b = find_sequence(p.cu, p.B, token, lane);
   if (b < 0 || b >= p.B || pos == -1) return;   // outside every sequence, or padding
@@ -231,26 +261,13 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_consta
   }
   const int first = p.cu[b], n = p.cu[b + 1] - first;
   if (token - first >= n) return;               // tables that do not ascend
-  const uint16_t* ks = p.k + token * p.ks[0] + li * 8;
-  const uint16_t* vs = p.v + token * p.vs[0] + li * 8;
-  uint4 kv[kIters], vv[kIters];
+  ln.load(p.rot, pos);
+  float wt[16];
+  load_weight(p.weight, ln.v, wt);
 #pragma unroll
   for (int r = 0; r < kIters; ++r) {
     const int h = h0 + r * kRows;
-    kv[r] = vv[r] = make_uint4(0u, 0u, 0u, 0u);
-    if (h < p.pg.heads) {
-      kv[r] = ld_stream(ks + h * p.ks[1]);
-      vv[r] = ld_stream(vs + h * p.vs[1]);
-    }
-  }
-  LaneRotation<kLanes> lr;
-  lr.load(p.rot, pos, li);
-  float wt[8];
-  load_weight(p.weight, li, wt);
-#pragma unroll
-  for (int r = 0; r < kIters; ++r) {
-    const int h = h0 + r * kRows;
-    const uint4 o = norm_rotate<DT, kLanes>(kv[r], p.norm, p.eps, p.weight != nullptr, wt, p.rot, lr);
+    norm_rotate<DT, D>(kw[r], p.norm, p.eps, p.weight != nullptr, wt, p.rot, ln);
     if (h >= p.pg.heads) continue;
     const int64_t e = int64_t(b) * p.pg.table_heads + (p.pg.table_heads > 1 ? h : 0);
     const int64_t row = int64_t(p.pg.len[e]) - n + (token - first);
@@ -263,9 +280,12 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_consta
     }
     const int64_t in_page = row & ((1 << p.pg.log2_page) - 1);
     const int64_t hp = p.pg.page_heads > 1 ? h : 0;
-    const int64_t at = ((((page * p.pg.page_heads + hp) << p.pg.log2_page) + in_page) * D) + li * 8;
-    *reinterpret_cast<uint4*>(p.k_pages + at) = o;
-    *reinterpret_cast<uint4*>(p.v_pages + at) = vv[r];
+    const int64_t at = (((page * p.pg.page_heads + hp) << p.pg.log2_page) + in_page) * D;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      *reinterpret_cast<uint4*>(p.k_pages + at + ln.v[i] * 8) = kw[r][i];
+      *reinterpret_cast<uint4*>(p.v_pages + at + ln.v[i] * 8) = vw[r][i];
+    }
   }
 }
 
@@ -288,12 +308,12 @@ static int make_rotation(Rotation* r, const float* rope, int rope_len, int rope_
 }
 
 
-static int launch_units(int64_t units, unsigned* grid) {
-  const int64_t g = (units + kRowThreads / 32 - 1) / (kRowThreads / 32);
-  if (g > INT32_MAX) return VARK_E_SHAPE;
-  *grid = unsigned(g);
-  return VARK_OK;
+// Grid of warps over (token, block of heads).
+static dim3 token_grid(int64_t tokens, int head_blocks) {
+  const int warps = kRowThreads / 32;
+  return dim3(unsigned((tokens + warps - 1) / warps), unsigned(head_blocks));
 }
+static int blocks_of(int heads, int per_block) { return (heads + per_block - 1) / per_block; }
 
 }  // namespace paged
 }  // namespace vark
@@ -313,11 +333,11 @@ extern "C" int vark_qk_norm_rope(int dtype, const uint16_t* q, const int64_t* q_
   int rc = check_common(dtype, D, norm, eps);
   if (rc) return rc;
   if (B < 0 || T < 0 || (q && Hq < 1) || (k && Hk < 1)) return VARK_E_SHAPE;
-  if (Hq > 65536 || Hk > 65536 || int64_t(B) * T > (int64_t(1) << 40)) return VARK_E_SHAPE;
+  if (Hq > 65536 || Hk > 65536 || int64_t(B) * T > INT32_MAX - kRowThreads) return VARK_E_SHAPE;
   NormRopeParams p;
   if ((rc = make_rotation(&p.rot, rope, rope_len, rope_dim, pairs, positions, D))) return rc;
   p.T = T > 0 ? T : 1;
-  p.tokens = int64_t(B) * T;
+  p.tokens = B * T;
   p.norm = norm;
   p.eps = eps;
   p.status = dev_status;
@@ -340,9 +360,8 @@ extern "C" int vark_qk_norm_rope(int dtype, const uint16_t* q, const int64_t* q_
   if (!aligned16(q_weight) || !aligned16(k_weight) || !aligned16(rope)) return VARK_E_ALIGN;
   if ((rc = check_device_sm100())) return rc;
   if (p.tokens == 0) return VARK_OK;
-  for (int i = 0; i < 2; ++i) p.blocks[i] = (p.t[i].heads + kHeadsPerWarp - 1) / kHeadsPerWarp;
-  unsigned grid;
-  if ((rc = launch_units(p.tokens * (p.blocks[0] + p.blocks[1]), &grid))) return rc;
+  p.q_blocks = blocks_of(p.t[0].heads, kQkHeads);
+  const dim3 grid = token_grid(p.tokens, p.q_blocks + blocks_of(p.t[1].heads, kQkHeads));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == VARK_BF16) {
     if (D == 128) norm_rope_kernel<VARK_BF16, 128><<<grid, kRowThreads, 0, st>>>(p);
@@ -366,7 +385,7 @@ extern "C" int vark_paged_append(int dtype, const uint16_t* k, const int64_t* k_
     return VARK_E_ARG;
   int rc = check_common(dtype, D, norm, eps);
   if (rc) return rc;
-  if (n_tokens < 0 || n_tokens > INT32_MAX || B < 0 || B > (1 << 24) || H < 1 || H > 65536) return VARK_E_SHAPE;
+  if (n_tokens < 0 || n_tokens > INT32_MAX - kRowThreads || B < 0 || B > (1 << 24) || H < 1 || H > 65536) return VARK_E_SHAPE;
   AppendParams p;
   if ((rc = make_rotation(&p.rot, rope, rope_len, rope_dim, pairs, positions, D))) return rc;
   if ((rc = make_pages(&p.pg, page_table, cache_len, n_pages, page_size, max_pages, H, head_pages))) return rc;
@@ -380,14 +399,12 @@ extern "C" int vark_paged_append(int dtype, const uint16_t* k, const int64_t* k_
   p.k_pages = k_pages; p.v_pages = v_pages;
   p.cu = cu_tokens;
   p.B = B;
-  p.tokens = n_tokens;
+  p.tokens = int(n_tokens);
   p.weight = k_weight;
   p.norm = norm;
   p.eps = eps;
   p.status = dev_status;
-  p.blocks = (H + kHeadsPerWarp - 1) / kHeadsPerWarp;
-  unsigned grid;
-  if ((rc = launch_units(n_tokens * p.blocks, &grid))) return rc;
+  const dim3 grid = token_grid(n_tokens, blocks_of(H, kKvHeads));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == VARK_BF16) {
     if (D == 128) append_kernel<VARK_BF16, 128><<<grid, kRowThreads, 0, st>>>(p);

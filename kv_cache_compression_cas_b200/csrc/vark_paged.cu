@@ -19,7 +19,14 @@
 namespace vark {
 namespace paged {
 
-constexpr int kRowThreads = 128;
+// Both kernels are bound by HBM at large sizes and by one chain of dependent
+// loads (position -> cosines) at small ones: the position is asked for before
+// the rows, rows are read and written as streams, and blocks are small so that
+// a finished one makes room at once.  Last scale of a batch of 8, 32768 tokens
+// of 16 + 16 heads: 95 us (5.65 TB/s); 128-thread blocks 102, the position
+// after the rows 111 with plain stores, 8 heads a warp 105, 6 blocks of 128 at
+// 80 registers 101.
+constexpr int kRowThreads = 64;
 
 struct Rotation {
   const float* table;       // [rope_len][2][dim / 2], or null
@@ -164,6 +171,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_rope_kernel(const __grid_con
   uint16_t* dst = t.dst + b * t.ds[0] + i * t.ds[1];
   Lane<D> ln;
   ln.place(p.rot, li);
+  const int pos = token_position(p.rot, token);
   uint4 w[kIters][2];
 #pragma unroll
   for (int r = 0; r < kIters; ++r) {
@@ -174,7 +182,6 @@ __global__ void __launch_bounds__(kRowThreads) norm_rope_kernel(const __grid_con
       w[r][1] = ld_stream(src + h * t.ss[2] + ln.v[1] * 8);
     }
   }
-  const int pos = token_position(p.rot, token);
   if (pos < 0) {
     if (pos == -2 && lane == 0) record(p.status, VARK_E_SHAPE);
     return;
@@ -187,8 +194,8 @@ __global__ void __launch_bounds__(kRowThreads) norm_rope_kernel(const __grid_con
     const int h = h0 + r * kRows;
     norm_rotate<DT, D>(w[r], p.norm, p.eps, t.weight != nullptr, wt, p.rot, ln);
     if (h < t.heads) {
-      *reinterpret_cast<uint4*>(dst + h * t.ds[2] + ln.v[0] * 8) = w[r][0];
-      *reinterpret_cast<uint4*>(dst + h * t.ds[2] + ln.v[1] * 8) = w[r][1];
+      __stcs(reinterpret_cast<uint4*>(dst + h * t.ds[2] + ln.v[0] * 8), w[r][0]);
+      __stcs(reinterpret_cast<uint4*>(dst + h * t.ds[2] + ln.v[1] * 8), w[r][1]);
     }
   }
 }
@@ -227,8 +234,10 @@ VARK_DEV int find_sequence(const int32_t* cu, int B, int64_t token, int lane) {
 
 constexpr int kKvHeads = 8;        // heads of a warp's token
 
+// 12 blocks an SM (80 registers): 47.8 us for 4 x 4096 tokens of 16 heads into
+// head pages (5.6 TB/s); unbounded (91 registers) 49.3, 4 heads a warp 51.4.
 template <int DT, int D>
-__global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kRowThreads, 12) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kLanes = D / 16, kRows = 32 / kLanes, kIters = (kKvHeads + kRows - 1) / kRows;
   const int lane = threadIdx.x & 31, li = lane % kLanes;
   const int token = int(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
@@ -236,7 +245,9 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_consta
   const int h0 = int(blockIdx.y) * kKvHeads + lane / kLanes;
   Lane<D> ln;
   ln.place(p.rot, li);
-  // The rows are asked for before the search: it takes a few dependent loads.
+  // The position first, and the rows before the search: each starts a chain
+  // of dependent loads.
+  const int pos = token_position(p.rot, token);
   const uint16_t* ks = p.k + token * p.ks[0];
   const uint16_t* vs = p.v + token * p.vs[0];
   uint4 kw[kIters][2], vw[kIters][2];
@@ -252,7 +263,6 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_consta
       }
     }
   }
-  const int pos = token_position(p.rot, token);
   const int b = find_sequence(p.cu, p.B, token, lane);
   if (b < 0 || b >= p.B || pos == -1) return;   // outside every sequence, or padding
   if (pos == -2) {
@@ -283,8 +293,8 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_consta
     const int64_t at = (((page * p.pg.page_heads + hp) << p.pg.log2_page) + in_page) * D;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      *reinterpret_cast<uint4*>(p.k_pages + at + ln.v[i] * 8) = kw[r][i];
-      *reinterpret_cast<uint4*>(p.v_pages + at + ln.v[i] * 8) = vw[r][i];
+      __stcs(reinterpret_cast<uint4*>(p.k_pages + at + ln.v[i] * 8), kw[r][i]);
+      __stcs(reinterpret_cast<uint4*>(p.v_pages + at + ln.v[i] * 8), vw[r][i]);
     }
   }
 }

@@ -13,6 +13,7 @@
 // into several shares leaves one partial (o, m, l) per CTA in the workspace; a
 // second, small kernel joins them.  Lengths live on the device: every CTA
 // finds its share with one scan over the sequence table.
+#include <atomic>
 #include <cstdlib>
 
 #include "vark_paged.cuh"
@@ -43,6 +44,13 @@ struct AttnParams {
   uint64_t wait_limit_ns;
   int withhold;            // test hook: slices a warp loads before it stops (-1: all)
 };
+
+// Dependent launches.  A call's two kernels, and calls that follow one another,
+// overlap at their ends: a kernel lets the next one start early, and the next
+// one waits for it (and all before it) before it touches what it may have
+// written.
+VARK_DEV void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+VARK_DEV void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ------------------------------------------------------------------ the plan
 // An entry is one row of the length table: a sequence (shared pages, all kv
@@ -83,8 +91,9 @@ VARK_DEV int64_t entry_units(const AttnParams& p, const Entry& x) {
 struct Share {
   int64_t total;           // units of the call
   int64_t u0, u1;          // this CTA's units
-  int e;                   // entry of the unit asked for, and its first unit
+  int e;                   // entry of the unit asked for, its first unit, and itself
   int64_t base;
+  Entry x;
 };
 
 VARK_DEV int64_t share_begin(int64_t total, int ctas, int c) { return total * c / ctas; }
@@ -96,12 +105,14 @@ VARK_DEV Share find_share(const AttnParams& p, int cta) {
   __shared__ int64_t warp_sum[THREADS / 32];
   __shared__ int64_t found_base;
   __shared__ int found_e;
+  __shared__ Entry found_x;
   const int E = p.B * p.pg.table_heads;
   const int chunk = (E + THREADS - 1) / THREADS;
   const int e0 = min(E, int(threadIdx.x) * chunk), e1 = min(E, e0 + chunk);
   int64_t sum = 0;
+  Entry x = {0, 0, 0, 0, 0, 0};
   for (int e = e0; e < e1; ++e) {
-    const Entry x = load_entry<R, KT>(p, e);
+    x = load_entry<R, KT>(p, e);
     sum += entry_units(p, x);
   }
   int64_t incl = sum;
@@ -131,11 +142,12 @@ VARK_DEV Share find_share(const AttnParams& p, int cta) {
   int64_t base = before + incl - sum;
   if (want >= base && want < base + sum) {
     for (int e = e0; e < e1; ++e) {
-      const Entry x = load_entry<R, KT>(p, e);
+      if (chunk > 1) x = load_entry<R, KT>(p, e);     // (else it is the one just read)
       const int64_t w = entry_units(p, x);
       if (want < base + w) {
         found_e = e;
         found_base = base;
+        found_x = x;
         break;
       }
       base += w;
@@ -144,6 +156,7 @@ VARK_DEV Share find_share(const AttnParams& p, int cta) {
   __syncthreads();
   s.e = found_e;
   s.base = found_base;
+  s.x = found_x;
   return s;
 }
 
@@ -160,7 +173,7 @@ struct Segments {
     base = s.base;
     u = s.u0;
     u1 = s.u1;
-    if (u < u1) x = load_entry<R, KT>(p, e);
+    x = s.x;
   }
   VARK_DEV bool next(const AttnParams& p) {
     if (u >= u1) return false;
@@ -314,6 +327,68 @@ VARK_DEV int seen_tiles(const AttnParams& p, const Segments<R, KT>& s) {
   return max(0, min(s.k1, (s.limit(p) + KT - 1) / KT) - s.k0);
 }
 
+// The loading warp of both kernels: the key and value tiles of a share's
+// segments, in order, into the ring of layout L (kRing, kTile, kPanel, kSlots,
+// kBar, kFull, kEmpty).  Lane i loads the tile's i-th box: 128 rows, or a page
+// where pages are smaller, whose number it asked for one tile ahead.
+template <int D, int R, typename L>
+VARK_DEV void load_tiles(const AttnParams& p, const Share& share, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                         uint32_t sbase, volatile int* abort_flag) {
+  const int lane = threadIdx.x & 31;
+  auto bar = [&](int i) { return sbase + L::kBar + 8u * uint32_t(i); };
+  const int box_log2 = min(p.pg.log2_page, 7);
+  const int boxes = kTileKT >> box_log2;
+  const int page_mask = (1 << p.pg.log2_page) - 1;
+  Segments<R, kTileKT> sg;
+  sg.start(p, share);
+  RingAt<L::kSlots> at = {0, 0};
+  int issued = 0;
+  bool ok = true;
+  while (ok && sg.next(p)) {
+    const int nt = seen_tiles(p, sg);
+    const int32_t* table = p.pg.table + int64_t(sg.e) * p.pg.max_pages;
+    const int head_row = (p.pg.page_heads > 1 ? sg.h : 0) << p.pg.log2_page;
+    int key = sg.k0 * kTileKT + (lane << box_log2);      // first key of this lane's box
+    auto page_of = [&](int k) { return lane < boxes && k < sg.x.len ? table[k >> p.pg.log2_page] : 0; };
+    int page = nt > 0 ? page_of(key) : 0;
+    for (int j = 0; ok && j < nt; ++j) {
+      const int next_page = j + 1 < nt ? page_of(key + kTileKT) : 0;
+      if (page < 0 || page >= p.pg.n_pages) {
+        record(p.status, VARK_E_SHAPE);
+        page = 0;           // in bounds; the call's outputs are void
+      }
+      const bool mine = lane < boxes && key < sg.x.len;
+      const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xffffffffu, mine))) << (box_log2 + (D == 128 ? 8 : 7));
+      const int row = head_row + (key & page_mask);
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        if (issued / 2 == p.withhold) ok = false;        // test hook: this tile never arrives
+        ok = ok && (issued < L::kSlots || mbar_wait(bar(L::kEmpty + at.slot), uint32_t(at.phase ^ 1), abort_flag,
+                                                    p.status, p.wait_limit_ns));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t full = bar(L::kFull + at.slot);
+        const uint32_t dst = sbase + L::kRing + at.slot * L::kTile + (lane << (box_log2 + 7));
+        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+        __syncwarp();
+        if (mine) {
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(dst + c * L::kPanel, which ? &tm_v : &tm_k, full, c * 64, row, page);
+        }
+        ++issued;
+        at.skip(1);
+      }
+      page = next_page;
+      key += kTileKT;
+    }
+  }
+  // Every load has landed before the CTA exits (at once unless a wait gave up).
+  volatile int no_abort = 0;
+  for (int i = max(0, issued - L::kSlots); i < issued; ++i)
+    mbar_wait(bar(L::kFull + i % L::kSlots), (i / L::kSlots) & 1, &no_abort, nullptr);
+}
+
 template <int DT, int D>
 __global__ void __launch_bounds__(kTileThreads, 1)
 tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -321,7 +396,6 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
   using L = TileSmem<D>;
   using Seg = Segments<kTileR, kTileKT>;
   using Ring = RingAt<L::kSlots>;
-  constexpr int NP = D / 64;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
@@ -333,7 +407,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
   };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_release();
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kSlots; ++i) {
       mbar_init(bar(L::kFull + i), 1);
@@ -351,6 +425,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
+  grid_wait();
   const Share share = find_share<kTileR, kTileKT, kTileThreads, false>(p, blockIdx.x);   // syncs the block
   if (share.u0 == share.u1) return;
   if (warp == 1) {
@@ -364,62 +439,8 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
 
   if (warp < 4) {
     setmaxnreg_dec56();
-    Seg sg;
-    sg.start(p, share);
     if (warp == 0) {
-      // -------------------------------------------------------- loader
-      const int box_log2 = min(p.pg.log2_page, 7);
-      const int boxes = kTileKT >> box_log2;          // pages a tile spans (1: a tile lies in one page)
-      Ring at = {0, 0};
-      int issued = 0;
-      bool ok = true;
-      while (ok && sg.next(p)) {
-        const int nt = seen_tiles(p, sg);
-        const int32_t* table = p.pg.table + int64_t(sg.e) * p.pg.max_pages;
-        auto page_at = [&](int j) {                   // page of this lane's box of tile j
-          const int key = (sg.k0 + j) * kTileKT + (lane << box_log2);
-          return lane < boxes && key < sg.x.len ? table[key >> p.pg.log2_page] : 0;
-        };
-        int page = nt > 0 ? page_at(0) : 0;
-        for (int j = 0; ok && j < nt; ++j) {
-          const int next_page = j + 1 < nt ? page_at(j + 1) : 0;
-          if (page < 0 || page >= p.pg.n_pages) {
-            record(p.status, VARK_E_SHAPE);
-            page = 0;           // in bounds; the call's outputs are void
-          }
-          const int key0 = (sg.k0 + j) * kTileKT;
-          const int used = min(boxes, (min(kTileKT, sg.x.len - key0) + (1 << box_log2) - 1) >> box_log2);
-          const int row = ((p.pg.page_heads > 1 ? sg.h : 0) << p.pg.log2_page) +
-                          ((key0 + (lane << box_log2)) & ((1 << p.pg.log2_page) - 1));
-          const uint32_t bytes = uint32_t(used) << (box_log2 + (D == 128 ? 8 : 7));
-#pragma unroll
-          for (int which = 0; which < 2; ++which) {
-            if (issued / 2 == p.withhold) ok = false;   // test hook: this tile never arrives
-            ok = ok && (issued < L::kSlots || wait(L::kEmpty + at.slot, at.phase ^ 1));
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            const uint32_t full = bar(L::kFull + at.slot);
-            const uint32_t dst = sbase + L::kRing + at.slot * L::kTile + (lane << (box_log2 + 7));
-            if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-            __syncwarp();
-            if (lane < used) {
-#pragma unroll
-              for (int c = 0; c < NP; ++c)
-                tma_load_3d(dst + c * L::kPanel, which ? &tm_v : &tm_k, full, c * 64, row, page);
-            }
-            ++issued;
-            at.skip(1);
-          }
-          page = next_page;
-        }
-      }
-      // Every load has landed before the CTA exits (at once unless a wait gave up).
-      volatile int no_abort = 0;
-      const int back = min(issued, L::kSlots);
-      for (int i = 0; i < back; ++i) {
-        const int k = issued - 1 - i;
-        mbar_wait(bar(L::kFull + k % L::kSlots), (k / L::kSlots) & 1, &no_abort, nullptr);
-      }
+      load_tiles<D, kTileR, L>(p, share, tm_k, tm_v, sbase, abort_flag);
     } else if (warp == 1) {
       // -------------------------------------------------------- MMA issue
       const uint32_t lead = elect_one();
@@ -442,6 +463,8 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         for (int k = 0; k < 8; ++k)
           mma_ts(lead, tmem + 256 + x * D, tmem + x * 128 + k * 8, b + k * (2048 >> 4), idesc_o, k > 0 ? 1u : acc);
       };
+      Seg sg;
+      sg.start(p, share);
       Ring kr = {0, 0}, vr = {1, 0};
       int q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
       bool ok = true;
@@ -696,15 +719,14 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
 
 // ------------------------------------------------------------------ rows kernel
 // Few rows a kv head (decoding, drafted tokens): bound by reading the keys and
-// values once.  8 warps, each with a ring of its own: a warp takes every eighth
-// 16-key slice of the CTA's key tiles, loads it by TMA (a slice lies within one
-// page; 128-byte swizzle) and works on it alone -- no barrier between warps
-// until an item ends, when the 8 partial results are added in shared memory.
+// values once.  The CTA's items are MT tiles of 16 rows; a loading warp fills a
+// ring of 128-key tiles, and 8 warps take 16 keys of every tile each, without a
+// barrier among them until an item ends, when their results are added in
+// shared memory.  The products run on mma.sync: 16 rows fill its tile where a
+// tcgen05 tile would be one eighth full.
+// (Warps 0-3 are the loader's group; three of them only hand their registers on.)
 constexpr int kRowWarps = 8;
-constexpr int kRowThreadsA = kRowWarps * 32;
-constexpr int kSlice = 16;
-constexpr int kRowKT = kRowWarps * kSlice;
-constexpr int kRowR = 16;
+constexpr int kRowThreads = kRowWarps * 32 + 128;
 
 template <int DT>
 VARK_DEV void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -732,336 +754,406 @@ VARK_DEV void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
                : "memory");
 }
 
-template <int D>
+template <int D, int MT>
 struct RowSmem {
-  static constexpr int kPanel = kSlice * 128;             // 16 rows x 64 channels
-  static constexpr int kHalf = (D / 64) * kPanel;         // one slice of K or V
-  static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = D == 128 ? 2 : 4;
-  static constexpr int kRing = 0;                         // [warp][stage]
-  static constexpr int kMergeStride = D + 8;              // floats; + 8 spreads the 8 rows of a store over the banks
-  static constexpr int kMerge = kRing + kRowWarps * kStages * kStage;           // [warp][16][stride] fp32
-  static constexpr int kML = kMerge + kRowWarps * kRowR * kMergeStride * 4;    // [warp][16][2] fp32
-  static constexpr int kBar = kML + kRowWarps * kRowR * 2 * 4;
-  static constexpr int kMisc = kBar + kRowWarps * kStages * 8;
+  static constexpr int kR = 16 * MT;
+  static constexpr int kPanel = kTileKT * 128;            // 128 rows x 64 channels
+  static constexpr int kTile = (D / 64) * kPanel;         // a tile's keys or values
+  static constexpr int kSlots = D == 128 ? 4 : 8;
+  static constexpr int kRing = 0;
+  static constexpr int kQPanel = kR * 128;
+  static constexpr int kQ = kRing + kSlots * kTile;
+  static constexpr int kStride = D + 8;                   // floats; + 8 spreads the 8 rows of a store over the banks
+  static constexpr int kMerge = kQ + (D / 64) * kQPanel;                         // [warp][16][stride] fp32
+  static constexpr int kML = kMerge + kRowWarps * 16 * kStride * 4;             // [warp][16][2] fp32
+  static constexpr int kRow = kML + kRowWarps * 16 * 2 * 4;                      // [kR] limit, [kR] scale
+  static constexpr int kBar = kRow + kR * 8;
+  static constexpr int kFull = 0, kEmpty = kSlots;        // barrier indices
+  static constexpr int kMisc = kBar + 2 * kSlots * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
+  static_assert(kAlloc + 2048 <= kMaxSmem, "shared memory");
 };
 
-template <int DT, int D>
-__global__ void __launch_bounds__(kRowThreadsA, 1)
+template <int DT, int D, int MT>
+__global__ void __launch_bounds__(kRowThreads, 1)
 rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
             const __grid_constant__ AttnParams p) {
-  using L = RowSmem<D>;
-  using Seg = Segments<kRowR, kRowKT>;
-  constexpr int NP = D / 64, KS = D / 16, NT = D / 8;
+  using L = RowSmem<D, MT>;
+  using Seg = Segments<L::kR, kTileKT>;
+  using Ring = RingAt<L::kSlots>;
+  constexpr int KS = D / 16, NT = D / 8, THREADS = kRowWarps * 32;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   float* merge = reinterpret_cast<float*>(smem + L::kMerge);
   float* ml = reinterpret_cast<float*>(smem + L::kML);
+  int* row_limit = reinterpret_cast<int*>(smem + L::kRow);
+  float* row_scale = reinterpret_cast<float*>(smem + L::kRow + L::kR * 4);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t4 = lane & 3;
-  const uint32_t ring = sbase + L::kRing + warp * L::kStages * L::kStage;
-  const uint32_t bar0 = sbase + L::kBar + warp * L::kStages * 8;
+  auto bar = [&](int i) { return sbase + L::kBar + 8u * uint32_t(i); };
+  const int warp = int(threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
+  const int tid = int(threadIdx.x) - 128;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_release();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kRowWarps * L::kStages; ++i) mbar_init(sbase + L::kBar + 8u * i, 1);
+    for (int i = 0; i < L::kSlots; ++i) {
+      mbar_init(bar(L::kFull + i), 1);
+      mbar_init(bar(L::kEmpty + i), kRowWarps);
+    }
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  const Share share = find_share<kRowR, kRowKT, kRowThreadsA, false>(p, blockIdx.x);   // syncs the block
+  grid_wait();
+  const Share share = find_share<L::kR, kTileKT, kRowThreads, false>(p, blockIdx.x);   // syncs the block
   if (share.u0 == share.u1) return;
+  if (warp < 0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
+    if (warp == -4) load_tiles<D, L::kR, L>(p, share, tm_k, tm_v, sbase, abort_flag);
+    return;
+  }
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 224;" ::: "memory");
+  auto sync = [&]() { named_bar_sync(1, THREADS); };
 
-  // The loading side of the warp: its next slice, and that slice's page.
-  Seg ps;
-  int p_slice = 0, p_end = 0, p_page = 0, p_count = 0;
-  bool p_more = true;
-  auto p_settle = [&]() {   // moves on to the next slice that exists and asks for its page
-    while (p_slice >= p_end) {
-      if (!ps.next(p)) {
-        p_more = false;
-        return;
-      }
-      p_slice = ps.k0 * kRowWarps + warp;
-      p_end = min(ps.k1 * kRowWarps, (ps.limit(p) + kSlice - 1) / kSlice);
-    }
-    p_page = p.pg.table[int64_t(ps.e) * p.pg.max_pages + ((p_slice * kSlice) >> p.pg.log2_page)];
-  };
-  auto p_issue = [&]() {
-    if (!p_more) return;
-    if (p_count == p.withhold) {
-      p_more = false;
-      return;
-    }
-    const int st = p_count % L::kStages;
-    if (lane == 0) {
-      int page = p_page;
-      if (page < 0 || page >= p.pg.n_pages) {
-        record(p.status, VARK_E_SHAPE);
-        page = 0;          // in bounds; the call's outputs are void
-      }
-      const int key0 = p_slice * kSlice;
-      const int row = ((p.pg.page_heads > 1 ? ps.h : 0) << p.pg.log2_page) + (key0 & ((1 << p.pg.log2_page) - 1));
-      const uint32_t bar = bar0 + 8u * st, dst = ring + st * L::kStage;
-      mbar_arrive_expect_tx(bar, L::kStage);
-#pragma unroll
-      for (int c = 0; c < NP; ++c) {
-        tma_load_3d(dst + c * L::kPanel, &tm_k, bar, c * 64, row, page);
-        tma_load_3d(dst + L::kHalf + c * L::kPanel, &tm_v, bar, c * 64, row, page);
-      }
-    }
-    ++p_count;
-    p_slice += kRowWarps;
-    p_settle();
-  };
-  ps.start(p, share);
-  p_settle();
-  for (int i = 0; i < L::kStages; ++i) p_issue();
-
-  // ldmatrix addresses of this lane (chunk index still to be xor-ed with the row)
+  const int g = lane >> 2, t4 = lane & 3;
+  // ldmatrix addresses of this lane: a row of a 16 x 16 block, and the 16-byte
+  // chunk of each 16-channel step within a panel (128-byte swizzle)
   const int lr = lane & 7, li = lane >> 3;
-  const uint32_t k_row = uint32_t(((li >> 1) * 8 + lr) * 128), k_chunk = uint32_t(li & 1);
-  const uint32_t v_row = uint32_t(((li & 1) * 8 + lr) * 128), v_chunk = uint32_t(li >> 1);
+  uint32_t k_off[4], v_off[4], q_off[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    k_off[i] = (warp * 16 + (li >> 1) * 8 + lr) * 128 + (((i * 2 + (li & 1)) ^ lr) << 4);
+    q_off[i] = ((li & 1) * 8 + lr) * 128 + (((i * 2 + (li >> 1)) ^ lr) << 4);
+    v_off[i] = warp * 16 * 128 + q_off[i];
+  }
 
   Seg cs;
   cs.start(p, share);
-  int c_count = 0;
+  Ring use = {0, 0};
   bool ok = true;
+  auto next_slot = [&]() -> uint32_t {      // waits for the next half of a tile
+    ok = ok && mbar_wait(bar(L::kFull + use.slot), uint32_t(use.phase), abort_flag, p.status, p.wait_limit_ns);
+    ok = __all_sync(0xffffffffu, ok);
+    return sbase + L::kRing + use.slot * L::kTile;
+  };
+  auto release = [&]() {                    // this warp is done with it
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(L::kEmpty + use.slot));
+    use.skip(1);
+  };
   while (cs.next(p)) {
-    // queries of the tile, as the A operand: rows g and g + 8 of this lane
-    const RowAt ra = row_at(p, cs, g), rb = row_at(p, cs, g + 8);
-    uint32_t qa[KS][4];
-    {
-      const uint16_t* qp = p.q + (ra.token < 0 ? 0 : ra.token * p.qs[0] + ra.head * p.qs[1]) + 2 * t4;
-      const uint16_t* qb = p.q + (rb.token < 0 ? 0 : rb.token * p.qs[0] + rb.head * p.qs[1]) + 2 * t4;
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        qa[k][0] = ra.token < 0 ? 0u : *reinterpret_cast<const uint32_t*>(qp + k * 16);
-        qa[k][1] = rb.token < 0 ? 0u : *reinterpret_cast<const uint32_t*>(qb + k * 16);
-        qa[k][2] = ra.token < 0 ? 0u : *reinterpret_cast<const uint32_t*>(qp + k * 16 + 8);
-        qa[k][3] = rb.token < 0 ? 0u : *reinterpret_cast<const uint32_t*>(qb + k * 16 + 8);
+    // The tile's queries, 128-byte swizzled, with what its rows see and scale
+    // by.  Under a negative temperature the query's sign is turned instead, so
+    // the largest score gives the largest logit; under 0 the query is 0.
+    for (int i = tid; i < L::kR * (D / 8); i += THREADS) {
+      const int r = i / (D / 8), ch = i % (D / 8);
+      const RowAt a = row_at(p, cs, r);
+      const float scale = p.scale_log2 * (p.tau != nullptr && a.token >= 0 ? p.tau[a.head] : 1.f);
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      if (a.token >= 0 && scale != 0.f)
+        w = *reinterpret_cast<const uint4*>(p.q + a.token * p.qs[0] + a.head * p.qs[1] + ch * 8);
+      const uint32_t flip = scale < 0.f ? 0x80008000u : 0u;
+      w.x ^= flip; w.y ^= flip; w.z ^= flip; w.w ^= flip;
+      st_shared_v4(sbase + L::kQ + (ch >> 3) * L::kQPanel + r * 128 + (((ch & 7) ^ (r & 7)) << 4), w);
+      if (ch == 0) {
+        row_limit[r] = a.limit;
+        row_scale[r] = scale == 0.f ? 1.f : fabsf(scale);
       }
     }
-    float scale[2] = {p.scale_log2, p.scale_log2};
-    if (p.tau != nullptr) {
-      if (ra.token >= 0) scale[0] *= p.tau[ra.head];
-      if (rb.token >= 0) scale[1] *= p.tau[rb.head];
+    sync();
+    int lim[MT][2];
+    float scale[MT][2], m[MT][2], top[MT][2], l[MT][2], o[MT][NT][4];   // top: m + the lag it may have
+    uint32_t qa[MT == 1 ? KS : 1][4];       // one tile: its A operand stays in registers
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        lim[mt][i] = row_limit[mt * 16 + g + 8 * i];
+        scale[mt][i] = row_scale[mt * 16 + g + 8 * i];
+        m[mt][i] = top[mt][i] = -INFINITY;
+        l[mt][i] = 0.f;
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[mt][n][i] = 0.f;
     }
-    const int lim[2] = {ra.limit, rb.limit};
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float o[NT][4];
+    if constexpr (MT == 1) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
-    const int end = min(cs.k1 * kRowWarps, (cs.limit(p) + kSlice - 1) / kSlice);
-    for (int slice = cs.k0 * kRowWarps + warp; slice < end; slice += kRowWarps) {
-      const int st = c_count % L::kStages;
-      ok = ok && mbar_wait(bar0 + 8u * st, (c_count / L::kStages) & 1, abort_flag, p.status, p.wait_limit_ns);
-      ok = __all_sync(0xffffffffu, ok);
+      for (int k = 0; k < KS; ++k) ldmatrix4(sbase + L::kQ + (k >> 2) * L::kQPanel + q_off[k & 3], qa[k]);
+    }
+    // keys that every row of the tile sees (the first row sees the fewest)
+    const int all_see = cs.tile * L::kR + L::kR <= cs.x.n * p.G ? row_limit[0] : 0;
+    const int nt = seen_tiles(p, cs);
+    int key0 = cs.k0 * kTileKT + warp * 16;
+    for (int j = 0; j < nt; ++j, key0 += kTileKT) {
+      const uint32_t sk = next_slot();
       if (!ok) break;
-      ++c_count;
-      const uint32_t sk = ring + st * L::kStage, sv = sk + L::kHalf;
-      const int key0 = slice * kSlice;
-      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      float s[MT][2][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[mt][n][i] = 0.f;
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         uint32_t b[4];
-        ldmatrix4(sk + (k >> 2) * L::kPanel + k_row + ((((k & 3) * 2 + k_chunk) ^ lr) << 4), b);
-        mma16816<DT>(s[0], qa[k], b[0], b[1]);
-        mma16816<DT>(s[1], qa[k], b[2], b[3]);
-      }
-      // scale, mask, running maximum
-      float f[2];
-      bool moved = false;
+        ldmatrix4(sk + k_off[k & 3] + (k >> 2) * L::kPanel, b);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float mx = -INFINITY;
+        for (int mt = 0; mt < MT; ++mt) {
+          uint32_t qf[4];
+          if constexpr (MT == 1) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int key = key0 + n * 8 + 2 * t4 + c;
-            float& x = s[n][2 * i + c];
-            x = key < lim[i] ? x * scale[i] : -INFINITY;
-            mx = fmaxf(mx, x);
+            for (int i = 0; i < 4; ++i) qf[i] = qa[k][i];
+          } else {
+            ldmatrix4(sbase + L::kQ + mt * 16 * 128 + (k >> 2) * L::kQPanel + q_off[k & 3], qf);
           }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        f[i] = 1.f;
-        if (mx > m[i] + kRescale || (m[i] == -INFINITY && mx > -INFINITY)) {
-          f[i] = ex2_approx(m[i] - mx);
-          m[i] = mx;
-          moved = true;
-        }
-        const float shift = m[i] == -INFINITY ? 0.f : m[i];
-        float sum = 0.f;
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float& x = s[n][2 * i + c];
-            x = ex2_approx(x - shift);
-            sum += x;
-          }
-        l[i] = l[i] * f[i] + sum;
-      }
-      if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          o[n][0] *= f[0];
-          o[n][1] *= f[0];
-          o[n][2] *= f[1];
-          o[n][3] *= f[1];
+          mma16816<DT>(s[mt][0], qf, b[0], b[1]);
+          mma16816<DT>(s[mt][1], qf, b[2], b[3]);
         }
       }
-      // the probabilities, rounded to the values' type, are the A operand of P V
-      const uint32_t pa[4] = {pack2<DT>(s[0][0], s[0][1]), pack2<DT>(s[0][2], s[0][3]),
-                              pack2<DT>(s[1][0], s[1][1]), pack2<DT>(s[1][2], s[1][3])};
+      release();
+      uint32_t pa[MT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        if (key0 + 16 > all_see) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (key0 + n * 8 + 2 * t4 + (i & 1) >= lim[mt][i >> 1]) s[mt][n][i] = -INFINITY;
+        }
+        // Against the running maximum, which may lag by 2^8: the four lanes of a
+        // row keep the same one and look for the new one together only when
+        // some score has passed it by more.
+        float mx[2];
+        bool past = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          mx[i] = fmaxf(fmax3(s[mt][0][2 * i], s[mt][0][2 * i + 1], s[mt][1][2 * i]), s[mt][1][2 * i + 1]) *
+                  scale[mt][i];
+          past |= mx[i] > top[mt][i];
+        }
+        if (__any_sync(0xffffffffu, past)) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+            if (mx[i] > top[mt][i]) {
+              const float f = ex2_approx(m[mt][i] - mx[i]);      // (the first time: 0)
+              m[mt][i] = mx[i];
+              top[mt][i] = mx[i] + kRescale;
+              l[mt][i] *= f;
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                o[mt][n][2 * i] *= f;
+                o[mt][n][2 * i + 1] *= f;
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float shift = m[mt][i] == -INFINITY ? 0.f : m[mt][i];
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              s[mt][n][2 * i + e] = ex2_approx(fmaf(s[mt][n][2 * i + e], scale[mt][i], -shift));
+          l[mt][i] += (s[mt][0][2 * i] + s[mt][0][2 * i + 1]) + (s[mt][1][2 * i] + s[mt][1][2 * i + 1]);
+        }
+        // the probabilities, rounded to the values' type, are the A operand of P V
+        pa[mt][0] = pack2<DT>(s[mt][0][0], s[mt][0][1]);
+        pa[mt][1] = pack2<DT>(s[mt][0][2], s[mt][0][3]);
+        pa[mt][2] = pack2<DT>(s[mt][1][0], s[mt][1][1]);
+        pa[mt][3] = pack2<DT>(s[mt][1][2], s[mt][1][3]);
+      }
+      const uint32_t sv = next_slot();
+      if (!ok) break;
       // rows behind the cache's end hold anything: 0 * NaN must not reach the sum
       const int left = cs.x.len - key0;
-      const bool tail = left < kSlice;
+      const bool tail = left < 16;
       const uint32_t keep0 = (2 * t4 < left ? 0xFFFFu : 0u) | (2 * t4 + 1 < left ? 0xFFFF0000u : 0u);
       const uint32_t keep1 = (2 * t4 + 8 < left ? 0xFFFFu : 0u) | (2 * t4 + 9 < left ? 0xFFFF0000u : 0u);
 #pragma unroll
       for (int c = 0; c < KS; ++c) {
         uint32_t b[4];
-        ldmatrix4_trans(sv + (c >> 2) * L::kPanel + v_row + ((((c & 3) * 2 + v_chunk) ^ lr) << 4), b);
+        ldmatrix4_trans(sv + v_off[c & 3] + (c >> 2) * L::kPanel, b);
         if (tail) {
           b[0] &= keep0;
           b[1] &= keep1;
           b[2] &= keep0;
           b[3] &= keep1;
         }
-        mma16816<DT>(o[2 * c], pa, b[0], b[1]);
-        mma16816<DT>(o[2 * c + 1], pa, b[2], b[3]);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          mma16816<DT>(o[mt][2 * c], pa[mt], b[0], b[1]);
+          mma16816<DT>(o[mt][2 * c + 1], pa[mt], b[2], b[3]);
+        }
       }
-      __syncwarp();        // every lane is done with the stage
-      p_issue();
+      release();
     }
-    // the 8 warps' results, relative to their own maxima
+    // the warps' results, each relative to its own maxima, 16 rows at a time
+    const bool whole = cs.k0 == 0 && cs.k1 == cs.x.key_tiles;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      const int r = g + 8 * i;
-      float* mo = merge + (warp * kRowR + r) * L::kMergeStride + 2 * t4;
+    for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-        *reinterpret_cast<float2*>(mo + n * 8) = make_float2(o[n][2 * i], o[n][2 * i + 1]);
-      if (t4 == 0) *reinterpret_cast<float2*>(ml + (warp * kRowR + r) * 2) = make_float2(m[i], l[i]);
-    }
-    __syncthreads();
-    {
-      const int r = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * (D / 16);
-      const RowAt a = row_at(p, cs, r);
-      if (a.token >= 0 && *abort_flag == 0) {
+      for (int i = 0; i < 2; ++i) {
+        l[mt][i] += __shfl_xor_sync(0xffffffffu, l[mt][i], 1);
+        l[mt][i] += __shfl_xor_sync(0xffffffffu, l[mt][i], 2);
+        const int r = g + 8 * i;
+        float* mo = merge + (warp * 16 + r) * L::kStride + 2 * t4;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          *reinterpret_cast<float2*>(mo + n * 8) = make_float2(o[mt][n][2 * i], o[mt][n][2 * i + 1]);
+        if (t4 == 0) *reinterpret_cast<float2*>(ml + (warp * 16 + r) * 2) = make_float2(m[mt][i], l[mt][i]);
+      }
+      sync();
+      for (int i = tid; i < 16 * (D / 8); i += THREADS) {
+        const int r = i / (D / 8), d0 = (i % (D / 8)) * 8;
+        const RowAt a = row_at(p, cs, mt * 16 + r);
+        if (a.token < 0 || *abort_flag != 0) continue;
         float top = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kRowWarps; ++w) top = fmaxf(top, ml[(w * kRowR + r) * 2]);
+        for (int w = 0; w < kRowWarps; ++w) top = fmaxf(top, ml[(w * 16 + r) * 2]);
         const float ref = top == -INFINITY ? 0.f : top;
         float sum = 0.f, acc[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
 #pragma unroll
         for (int w = 0; w < kRowWarps; ++w) {
-          const float wgt = ex2_approx(ml[(w * kRowR + r) * 2] - ref);
-          sum = fmaf(ml[(w * kRowR + r) * 2 + 1], wgt, sum);
-          const float* mo = merge + (w * kRowR + r) * L::kMergeStride + d0;
+          const float2 v = *reinterpret_cast<const float2*>(ml + (w * 16 + r) * 2);
+          const float wgt = ex2_approx(v.x - ref);
+          sum = fmaf(v.y, wgt, sum);
+          const float* mo = merge + (w * 16 + r) * L::kStride + d0;
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) acc[i] = fmaf(mo[i], wgt, acc[i]);
+          for (int e = 0; e < 8; ++e) acc[e] = fmaf(mo[e], wgt, acc[e]);
         }
-        const bool whole = cs.k0 == 0 && cs.k1 == cs.x.key_tiles;
-        if (whole && D == 128) {
+        if (whole) {
           store_row8<DT>(p, a, d0, acc, top, sum);
-        } else if (whole) {
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          *reinterpret_cast<uint2*>(p.out + a.token * p.os[0] + a.head * p.os[1] + d0) =
-              make_uint2(pack2<DT>(acc[0] * inv, acc[1] * inv), pack2<DT>(acc[2] * inv, acc[3] * inv));
-          if (d0 == 0 && p.lse != nullptr)
-            p.lse[int64_t(a.token) * p.Hq + a.head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
         } else {
-          const int64_t slot = (int64_t(blockIdx.x) * 2 + (cs.k0 == 0 ? 1 : 0)) * kRowR + r;
-#pragma unroll
-          for (int i = 0; i < D / 16; i += 4)
-            *reinterpret_cast<float4*>(p.part_o + slot * D + d0 + i) =
-                make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+          const int64_t slot = (int64_t(blockIdx.x) * 2 + (cs.k0 == 0 ? 1 : 0)) * L::kR + mt * 16 + r;
+          float4* to = reinterpret_cast<float4*>(p.part_o + slot * D + d0);
+          to[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+          to[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
           if (d0 == 0) *reinterpret_cast<float2*>(p.part_ml + slot * 2) = make_float2(top, sum);
         }
       }
+      sync();
     }
-    __syncthreads();
   }
-  // Loads that nothing consumed (only after a wait that gave up) land before the CTA exits.
-  volatile int no_abort = 0;
-  for (; c_count < p_count; ++c_count)
-    mbar_wait(bar0 + 8u * (c_count % L::kStages), (c_count / L::kStages) & 1, &no_abort, nullptr);
 }
 
 // Joins the partial results of the item that starts in share c = blockIdx.x
-// and ends in a later one; blockIdx.y: 16 rows of the tile.
+// and ends in a later one.  blockIdx.y: 64 of the tile's rows, taken 16 at a
+// time; where fewer rows exist, the threads of the others share the partials.
 template <int DT, int D, int R, int KT>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int kChunk = D / 8;                     // threads of a row, 8 channels each
+  constexpr int kSlotsT = 256 / kChunk;             // (row, part) slots
+  __shared__ float red[kSlotsT][D + 4];
+  __shared__ float red_ml[kSlotsT][2];
   const int c = blockIdx.x;
+  grid_release();
   const Share s = find_share<R, KT, 256, true>(p, c);
+  const Entry x = s.x;
+  const int64_t off = s.u1 - 1 - s.base;
+  const int item = s.u0 == s.u1 ? 0 : int(off / x.key_tiles);
+  const int64_t begin = s.base + int64_t(item) * x.key_tiles, end = begin + x.key_tiles;
   // Every CTA waits, also those without an item: the launch after this one
   // may count on the attention kernel's end.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (s.u0 == s.u1) return;
-  const Entry x = load_entry<R, KT>(p, s.e);
-  const int64_t off = s.u1 - 1 - s.base;
-  const int item = int(off / x.key_tiles);
-  const int64_t begin = s.base + int64_t(item) * x.key_tiles, end = begin + x.key_tiles;
-  if (begin < s.u0 || end <= s.u1) return;
+  grid_wait();
+  if (s.u0 == s.u1 || begin < s.u0 || end <= s.u1) return;
+  if (*reinterpret_cast<volatile int32_t*>(p.status) != 0) return;
   Segments<R, KT> seg;
   seg.e = s.e;
   seg.x = x;
   seg.h = p.pg.table_heads > 1 ? s.e % p.pg.heads : item / x.row_tiles;
   seg.tile = item % x.row_tiles;
-  const int r = blockIdx.y * 16 + (threadIdx.x >> 4), d0 = (threadIdx.x & 15) * (D / 16);
-  const RowAt a = row_at(p, seg, r);
   // the shares that hold a part: c, c + 1, ... while they start before the item ends
   const int ctas = int(min(int64_t(kCtas), s.total));
   int last = c + 1;
   while (last + 1 < ctas && share_begin(s.total, ctas, last + 1) < end) ++last;
-  if (a.token < 0 || *reinterpret_cast<volatile int32_t*>(p.status) != 0) return;
-  auto slot = [&](int i) { return (int64_t(i) * 2 + (i == c ? 1 : 0)) * R + r; };
-  float top = -INFINITY;
-  for (int i = c; i <= last; ++i) top = fmaxf(top, p.part_ml[slot(i) * 2]);
-  const float ref = top == -INFINITY ? 0.f : top;
-  float sum = 0.f, acc[8];
+  const int rows = min(R, x.n * p.G - seg.tile * R);
+  const int d0 = (threadIdx.x % kChunk) * 8, slot = threadIdx.x / kChunk;
+  for (int r0 = blockIdx.y * 64; r0 < min(rows, int(blockIdx.y) * 64 + 64); r0 += kSlotsT) {
+    int width = 1;                                   // slots a part takes
+    while (width < min(kSlotsT, rows - r0)) width *= 2;
+    const int parts = kSlotsT / width, r = r0 + slot % width;
+    float top = -INFINITY, sum = 0.f, acc[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-#pragma unroll 4
-  for (int i = c; i <= last; ++i) {
-    const float2 v = *reinterpret_cast<const float2*>(p.part_ml + slot(i) * 2);
-    const float wgt = ex2_approx(v.x - ref);
-    sum = fmaf(v.y, wgt, sum);
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    if (r < rows) {
+      auto at = [&](int i) { return (int64_t(i) * 2 + (i == c ? 1 : 0)) * R + r; };
+      constexpr int kBatch = 3;                      // partials in flight a thread
+      for (int i0 = c + slot / width; i0 <= last; i0 += kBatch * parts) {
+        float2 v[kBatch];
+        float4 w[kBatch][2];
 #pragma unroll
-    for (int d = 0; d < D / 16; d += 4) {
-      const float4 w = *reinterpret_cast<const float4*>(p.part_o + slot(i) * D + d0 + d);
-      acc[d] = fmaf(w.x, wgt, acc[d]);
-      acc[d + 1] = fmaf(w.y, wgt, acc[d + 1]);
-      acc[d + 2] = fmaf(w.z, wgt, acc[d + 2]);
-      acc[d + 3] = fmaf(w.w, wgt, acc[d + 3]);
+        for (int k = 0; k < kBatch; ++k) {
+          const int i = i0 + k * parts;
+          v[k] = make_float2(-INFINITY, 0.f);
+          w[k][0] = w[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i <= last) {
+            v[k] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + at(i) * 2));
+            w[k][0] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at(i) * D + d0));
+            w[k][1] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at(i) * D + d0 + 4));
+          }
+        }
+        float big = top;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) big = fmaxf(big, v[k].x);
+        const float ref = big == -INFINITY ? 0.f : big;
+        const float old = ex2_approx(top - ref);
+        top = big;
+        sum *= old;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] *= old;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const float wgt = ex2_approx(v[k].x - ref);
+          sum = fmaf(v[k].y, wgt, sum);
+          const float z[8] = {w[k][0].x, w[k][0].y, w[k][0].z, w[k][0].w, w[k][1].x, w[k][1].y, w[k][1].z, w[k][1].w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] = fmaf(z[e], wgt, acc[e]);
+        }
+      }
     }
-  }
-  if constexpr (D == 128) {
-    store_row8<DT>(p, a, d0, acc, top, sum);
-  } else {
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    *reinterpret_cast<uint2*>(p.out + a.token * p.os[0] + a.head * p.os[1] + d0) =
-        make_uint2(pack2<DT>(acc[0] * inv, acc[1] * inv), pack2<DT>(acc[2] * inv, acc[3] * inv));
-    if (d0 == 0 && p.lse != nullptr)
-      p.lse[int64_t(a.token) * p.Hq + a.head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    if (parts > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < 8; e += 4)
+        *reinterpret_cast<float4*>(&red[slot][d0 + e]) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+      if (d0 == 0) {
+        red_ml[slot][0] = top;
+        red_ml[slot][1] = sum;
+      }
+      __syncthreads();
+      if (slot < width) {
+        float big = top;
+        for (int q = 1; q < parts; ++q) big = fmaxf(big, red_ml[slot + q * width][0]);
+        const float ref = big == -INFINITY ? 0.f : big;
+        const float own = ex2_approx(top - ref);
+        top = big;
+        sum *= own;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] *= own;
+        for (int q = 1; q < parts; ++q) {
+          const float wgt = ex2_approx(red_ml[slot + q * width][0] - ref);
+          sum = fmaf(red_ml[slot + q * width][1], wgt, sum);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] = fmaf(red[slot + q * width][d0 + e], wgt, acc[e]);
+        }
+      }
+    }
+    if (slot < width && r < rows) store_row8<DT>(p, row_at(p, seg, r), d0, acc, top, sum);
   }
 }
 
 // ------------------------------------------------------------------ host side
+constexpr int kPairRows = 12;      // mean rows a (sequence, kv head) above which two row tiles go together
 constexpr int kTileRows = 32;      // mean rows a (sequence, kv head) above which the tiles kernel runs
 constexpr int kWaves = 4;          // items for this many rounds of the device: no split along the keys
 
@@ -1085,57 +1177,73 @@ static int encode_pages(CUtensorMap* m, const uint16_t* base, const Pages& pg, i
   return encode_bf16_map(m, base, 3, dims, strides, uint32_t(box_rows));   // 16-bit elements, copied as they are
 }
 
-// The join starts while the attention kernel still runs (it finds its share
-// meanwhile) and waits for it before it reads a partial.
-template <typename K>
-static int launch_join(K kern, dim3 grid, const AttnParams& p, cudaStream_t st) {
+// Launch that may start before the kernels ahead of it have ended (see
+// grid_wait).
+template <typename K, typename... A>
+static int launch_early(K kern, dim3 grid, int threads, int smem, cudaStream_t st, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = size_t(smem);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? VARK_OK : VARK_E_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess) return VARK_OK;
+  cudaGetLastError();
+  return VARK_E_CUDA;
+}
+
+// Lets a kernel use more than 48 KB of shared memory; asked for once a device.
+template <typename K>
+static int allow_smem(K kern, int smem, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return VARK_E_CUDA;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (done->load(std::memory_order_relaxed) & bit) return VARK_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+    cudaGetLastError();
+    return VARK_E_CUDA;
+  }
+  if (dev < 64) done->fetch_or(bit, std::memory_order_relaxed);
+  return VARK_OK;
 }
 
 template <int DT, int D>
 static int launch_tiles(const CUtensorMap& k, const CUtensorMap& v, const AttnParams& p, int64_t grid,
                         cudaStream_t st) {
-  auto kern = tiles_kernel<DT, D>;
-  const int smem = TileSmem<D>::kAlloc;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
-    cudaGetLastError();
-    return VARK_E_CUDA;
-  }
-  kern<<<unsigned(grid), kTileThreads, smem, st>>>(k, v, p);
-  if (cudaGetLastError() != cudaSuccess) return VARK_E_CUDA;
-  if (!p.split) return VARK_OK;
-  const int rc = launch_join(join_kernel<DT, D, kTileR, kTileKT>, dim3(kCtas, kTileR / 16), p, st);
-  if (rc) cudaGetLastError();
-  return rc;
+  static std::atomic<uint64_t> done{0};
+  constexpr int smem = TileSmem<D>::kAlloc;
+  int rc = allow_smem(tiles_kernel<DT, D>, smem, &done);
+  if (!rc) rc = launch_early(tiles_kernel<DT, D>, dim3(unsigned(grid)), kTileThreads, smem, st, k, v, p);
+  if (rc || !p.split) return rc;
+  return launch_early(join_kernel<DT, D, kTileR, kTileKT>, dim3(kCtas, kTileR / 64), 256, 0, st, p);
 }
 
-template <int DT, int D>
+template <int DT, int D, int MT>
 static int launch_rows(const CUtensorMap& k, const CUtensorMap& v, const AttnParams& p, cudaStream_t st) {
-  auto kern = rows_kernel<DT, D>;
-  const int smem = RowSmem<D>::kAlloc;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
-    cudaGetLastError();
-    return VARK_E_CUDA;
-  }
-  kern<<<kCtas, kRowThreadsA, smem, st>>>(k, v, p);
-  if (cudaGetLastError() != cudaSuccess) return VARK_E_CUDA;
-  const int rc = launch_join(join_kernel<DT, D, kRowR, kRowKT>, dim3(kCtas, kRowR / 16), p, st);
-  if (rc) cudaGetLastError();
-  return rc;
+  static std::atomic<uint64_t> done{0};
+  constexpr int smem = RowSmem<D, MT>::kAlloc;
+  int rc = allow_smem(rows_kernel<DT, D, MT>, smem, &done);
+  if (!rc) rc = launch_early(rows_kernel<DT, D, MT>, dim3(kCtas), kRowThreads, smem, st, k, v, p);
+  if (rc) return rc;
+  return launch_early(join_kernel<DT, D, 16 * MT, kTileKT>, dim3(kCtas), 256, 0, st, p);
+}
+
+template <int DT>
+static int launch(int D, int rows, const CUtensorMap& k, const CUtensorMap& v, const AttnParams& p, int64_t grid,
+                  cudaStream_t st) {
+  if (rows == kTileR)
+    return D == 128 ? launch_tiles<DT, 128>(k, v, p, grid, st) : launch_tiles<DT, 64>(k, v, p, grid, st);
+  if (rows == 32) return D == 128 ? launch_rows<DT, 128, 2>(k, v, p, st) : launch_rows<DT, 64, 2>(k, v, p, st);
+  return D == 128 ? launch_rows<DT, 128, 1>(k, v, p, st) : launch_rows<DT, 64, 1>(k, v, p, st);
 }
 
 // How a call is run, from its shapes alone (the lengths are on the device).
 struct Variant {
-  bool tiles;              // tensor-core tiles of 256 rows, or rows of 16
+  int rows;                // rows of an item: 256 (tcgen05 tiles), 32 or 16
   bool split;
   int64_t items;           // at most this many items
 };
@@ -1143,15 +1251,15 @@ static Variant choose(int64_t n_tokens, int B, int Hq, int Hkv) {
   const int64_t G = Hq / Hkv;
   Variant v;
   const int64_t rows = n_tokens * G;                  // of a kv head, over all sequences
-  v.tiles = rows > int64_t(B) * kTileRows;
-  v.items = (rows / kTileR + B) * Hkv;
-  v.split = !v.tiles || rows / kTileR * Hkv < int64_t(kWaves) * kCtas;
+  v.rows = rows > int64_t(B) * kTileRows ? kTileR : rows > int64_t(B) * kPairRows ? 32 : 16;
+  v.items = (rows / v.rows + B) * Hkv;
+  v.split = v.rows < kTileR || rows / kTileR * Hkv < int64_t(kWaves) * kCtas;
   return v;
 }
 
 static int64_t workspace_bytes_for(const Variant& v, int D) {
   if (!v.split) return 16;
-  return int64_t(kCtas) * 2 * (v.tiles ? kTileR : kRowR) * (D + 2) * 4;
+  return int64_t(kCtas) * 2 * v.rows * (D + 2) * 4;
 }
 
 }  // namespace paged
@@ -1203,23 +1311,15 @@ extern "C" int vark_paged_attention(int dtype, const uint16_t* q, const int64_t*
   if (var.items > INT32_MAX) return VARK_E_SHAPE;
   p.split = var.split;
   p.part_ml = static_cast<float*>(workspace);
-  p.part_o = p.part_ml + int64_t(kCtas) * 2 * (var.tiles ? kTileR : kRowR) * 2;
+  p.part_o = p.part_ml + int64_t(kCtas) * 2 * var.rows * 2;
   p.status = dev_status;
   test_hooks(p);
-  const int box = var.tiles ? (page_size < kTileKT ? page_size : kTileKT) : kSlice;
+  const int box = page_size < kTileKT ? page_size : kTileKT;
   CUtensorMap tk, tv;
   if ((rc = encode_pages(&tk, k_pages, p.pg, D, box))) return rc;
   if ((rc = encode_pages(&tv, v_pages, p.pg, D, box))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (var.tiles) {
-    const int64_t grid = var.split ? kCtas : var.items;
-    if (dtype == VARK_BF16)
-      return D == 128 ? launch_tiles<VARK_BF16, 128>(tk, tv, p, grid, st)
-                      : launch_tiles<VARK_BF16, 64>(tk, tv, p, grid, st);
-    return D == 128 ? launch_tiles<VARK_FP16, 128>(tk, tv, p, grid, st)
-                    : launch_tiles<VARK_FP16, 64>(tk, tv, p, grid, st);
-  }
-  if (dtype == VARK_BF16)
-    return D == 128 ? launch_rows<VARK_BF16, 128>(tk, tv, p, st) : launch_rows<VARK_BF16, 64>(tk, tv, p, st);
-  return D == 128 ? launch_rows<VARK_FP16, 128>(tk, tv, p, st) : launch_rows<VARK_FP16, 64>(tk, tv, p, st);
+  const int64_t grid = var.split ? kCtas : var.items;
+  return dtype == VARK_BF16 ? launch<VARK_BF16>(D, var.rows, tk, tv, p, grid, st)
+                            : launch<VARK_FP16>(D, var.rows, tk, tv, p, grid, st);
 }

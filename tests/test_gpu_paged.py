@@ -193,6 +193,10 @@ ATTENTION = [
     ([1] * 40, list(range(3, 43)), 16, 1, 128, 16, False, True),
     ([260], [260], 2, 1, 128, 64, False, True),
     ([300, 7], [1000, 600], 3, 1, 128, 128, False, False),
+    ([5, 9, 12], [200, 9, 70], 4, 2, 64, 16, False, True),
+    ([6, 3, 0, 7], [500, 90, 5, 40], 16, 4, 128, 256, False, False),
+    ([9, 8], [[700, 9], [5, 33]], 4, 2, 64, 32, True, True),
+    ([200, 200], [200, 1500], 4, 4, 64, 16, False, True),
 ]
 
 

@@ -83,9 +83,12 @@ VARK_DEV Entry load_entry(const AttnParams& p, int e) {
   return x;
 }
 
-// Units of work: key tiles (split), or whole items.
+// Units of work (split): an item's key tiles, and one ahead of them for what
+// starting and finishing it costs (about a tile's time: without it the shares
+// with many short sequences ended last).  Not split: whole items.
+VARK_DEV int item_units(const Entry& x) { return x.key_tiles + 1; }
 VARK_DEV int64_t entry_units(const AttnParams& p, const Entry& x) {
-  return p.split ? int64_t(x.items) * x.key_tiles : x.items;
+  return p.split ? int64_t(x.items) * item_units(x) : x.items;
 }
 
 struct Share {
@@ -186,10 +189,13 @@ struct Segments {
     k0 = 0;
     k1 = x.key_tiles;
     if (p.split) {
-      item = int(off / x.key_tiles);
-      k0 = int(off - int64_t(item) * x.key_tiles);
-      k1 = int(min(int64_t(x.key_tiles), k0 + (u1 - u)));
-      u += k1 - k0;
+      item = int(off / item_units(x));
+      const int pos = int(off - int64_t(item) * item_units(x));
+      const int take = int(min(int64_t(item_units(x) - pos), u1 - u));
+      k0 = max(0, pos - 1);
+      k1 = pos + take - 1;
+      u += take;
+      if (k1 == 0) return false;     // the share ends ahead of the item's first tile
     } else {
       ++u;
     }
@@ -782,6 +788,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   using Seg = Segments<L::kR, kTileKT>;
   using Ring = RingAt<L::kSlots>;
   constexpr int KS = D / 16, NT = D / 8, THREADS = kRowWarps * 32;
+  constexpr bool kQRegs = MT * KS <= 8;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
@@ -828,8 +835,6 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     v_off[i] = warp * 16 * 128 + q_off[i];
   }
 
-  Seg cs;
-  cs.start(p, share);
   Ring use = {0, 0};
   bool ok = true;
   auto next_slot = [&]() -> uint32_t {      // waits for the next half of a tile
@@ -842,29 +847,56 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     if (lane == 0) mbar_arrive(bar(L::kEmpty + use.slot));
     use.skip(1);
   };
-  while (cs.next(p)) {
-    // The tile's queries, 128-byte swizzled, with what its rows see and scale
-    // by.  Under a negative temperature the query's sign is turned instead, so
-    // the largest score gives the largest logit; under 0 the query is 0.
-    for (int i = tid; i < L::kR * (D / 8); i += THREADS) {
-      const int r = i / (D / 8), ch = i % (D / 8);
-      const RowAt a = row_at(p, cs, r);
-      const float scale = p.scale_log2 * (p.tau != nullptr && a.token >= 0 ? p.tau[a.head] : 1.f);
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (a.token >= 0 && scale != 0.f)
-        w = *reinterpret_cast<const uint4*>(p.q + a.token * p.qs[0] + a.head * p.qs[1] + ch * 8);
-      const uint32_t flip = scale < 0.f ? 0x80008000u : 0u;
+  // The tile's queries: asked for while the segment before is worked on, then
+  // stored 128-byte swizzled with what their rows see and scale by.  Under a
+  // negative temperature the query's sign is turned instead, so the largest
+  // score gives the largest logit; under 0 the query is 0.
+  constexpr int NQ = (L::kR * (D / 8) + THREADS - 1) / THREADS;
+  uint4 qw[NQ];
+  int q_limit[NQ];
+  float q_scale[NQ];
+  auto fetch = [&](const Seg& sg) {
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      const int r = (tid + n * THREADS) / (D / 8), ch = tid % (D / 8);
+      const RowAt a = row_at(p, sg, r);
+      q_limit[n] = a.limit;
+      q_scale[n] = p.scale_log2;
+      qw[n] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < L::kR && a.token >= 0) {
+        if (p.tau != nullptr) q_scale[n] *= p.tau[a.head];
+        qw[n] = *reinterpret_cast<const uint4*>(p.q + a.token * p.qs[0] + a.head * p.qs[1] + ch * 8);
+      }
+    }
+  };
+  auto put = [&]() {
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      const int r = (tid + n * THREADS) / (D / 8), ch = tid % (D / 8);
+      if (r >= L::kR) continue;
+      const uint32_t flip = q_scale[n] < 0.f ? 0x80008000u : 0u;
+      uint4 w = q_scale[n] == 0.f ? make_uint4(0u, 0u, 0u, 0u) : qw[n];
       w.x ^= flip; w.y ^= flip; w.z ^= flip; w.w ^= flip;
       st_shared_v4(sbase + L::kQ + (ch >> 3) * L::kQPanel + r * 128 + (((ch & 7) ^ (r & 7)) << 4), w);
       if (ch == 0) {
-        row_limit[r] = a.limit;
-        row_scale[r] = scale == 0.f ? 1.f : fabsf(scale);
+        row_limit[r] = q_limit[n];
+        row_scale[r] = q_scale[n] == 0.f ? 1.f : fabsf(q_scale[n]);
       }
     }
+  };
+  Seg cs, ahead;
+  ahead.start(p, share);
+  bool more = ahead.next(p);
+  if (more) fetch(ahead);
+  while (more) {
+    put();
+    cs = ahead;
     sync();
+    more = ahead.next(p);
+    if (more) fetch(ahead);
     int lim[MT][2];
     float scale[MT][2], m[MT][2], top[MT][2], l[MT][2], o[MT][NT][4];   // top: m + the lag it may have
-    uint32_t qa[MT == 1 ? KS : 1][4];       // one tile: its A operand stays in registers
+    uint32_t qa[kQRegs ? MT * KS : 1][4];   // the A operand, where it fits the registers
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -879,9 +911,12 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[mt][n][i] = 0.f;
     }
-    if constexpr (MT == 1) {
+    if constexpr (kQRegs) {
 #pragma unroll
-      for (int k = 0; k < KS; ++k) ldmatrix4(sbase + L::kQ + (k >> 2) * L::kQPanel + q_off[k & 3], qa[k]);
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+          ldmatrix4(sbase + L::kQ + mt * 16 * 128 + (k >> 2) * L::kQPanel + q_off[k & 3], qa[mt * KS + k]);
     }
     // keys that every row of the tile sees (the first row sees the fewest)
     const int all_see = cs.tile * L::kR + L::kR <= cs.x.n * p.G ? row_limit[0] : 0;
@@ -890,13 +925,15 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     for (int j = 0; j < nt; ++j, key0 += kTileKT) {
       const uint32_t sk = next_slot();
       if (!ok) break;
-      float s[MT][2][4];
+      // two sums a score, over even and odd 16-channel steps: half the chain of
+      // dependent MMAs
+      float s[MT][2][4], s2[MT][2][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[mt][n][i] = 0.f;
+          for (int i = 0; i < 4; ++i) s[mt][n][i] = s2[mt][n][i] = 0.f;
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         uint32_t b[4];
@@ -904,47 +941,56 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           uint32_t qf[4];
-          if constexpr (MT == 1) {
+          if constexpr (kQRegs) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) qf[i] = qa[k][i];
+            for (int i = 0; i < 4; ++i) qf[i] = qa[mt * KS + k][i];
           } else {
             ldmatrix4(sbase + L::kQ + mt * 16 * 128 + (k >> 2) * L::kQPanel + q_off[k & 3], qf);
           }
-          mma16816<DT>(s[mt][0], qf, b[0], b[1]);
-          mma16816<DT>(s[mt][1], qf, b[2], b[3]);
+          mma16816<DT>((k & 1) ? s2[mt][0] : s[mt][0], qf, b[0], b[1]);
+          mma16816<DT>((k & 1) ? s2[mt][1] : s[mt][1], qf, b[2], b[3]);
         }
       }
       release();
-      uint32_t pa[MT][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        if (key0 + 16 > all_see) {
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[mt][n][i] += s2[mt][n][i];
+      if (key0 + 16 > all_see) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               if (key0 + n * 8 + 2 * t4 + (i & 1) >= lim[mt][i >> 1]) s[mt][n][i] = -INFINITY;
-        }
-        // Against the running maximum, which may lag by 2^8: the four lanes of a
-        // row keep the same one and look for the new one together only when
-        // some score has passed it by more.
-        float mx[2];
-        bool past = false;
+      }
+      // Against the running maximum, which may lag by 2^8: the four lanes of a
+      // row keep the same one and look for the new one together only when
+      // some score has passed it by more.
+      float mx[MT][2];
+      bool past = false;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          mx[i] = fmaxf(fmax3(s[mt][0][2 * i], s[mt][0][2 * i + 1], s[mt][1][2 * i]), s[mt][1][2 * i + 1]) *
-                  scale[mt][i];
-          past |= mx[i] > top[mt][i];
+          mx[mt][i] = fmaxf(fmax3(s[mt][0][2 * i], s[mt][0][2 * i + 1], s[mt][1][2 * i]), s[mt][1][2 * i + 1]) *
+                      scale[mt][i];
+          past |= mx[mt][i] > top[mt][i];
         }
-        if (__any_sync(0xffffffffu, past)) {
+      if (__any_sync(0xffffffffu, past)) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-            if (mx[i] > top[mt][i]) {
-              const float f = ex2_approx(m[mt][i] - mx[i]);      // (the first time: 0)
-              m[mt][i] = mx[i];
-              top[mt][i] = mx[i] + kRescale;
+            float v = fmaxf(mx[mt][i], __shfl_xor_sync(0xffffffffu, mx[mt][i], 1));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+            if (v > top[mt][i]) {
+              const float f = ex2_approx(m[mt][i] - v);          // (the first time: 0)
+              m[mt][i] = v;
+              top[mt][i] = v + kRescale;
               l[mt][i] *= f;
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
@@ -953,7 +999,10 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
               }
             }
           }
-        }
+      }
+      uint32_t pa[MT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float shift = m[mt][i] == -INFINITY ? 0.f : m[mt][i];
@@ -1060,12 +1109,12 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnP
   const Share s = find_share<R, KT, 256, true>(p, c);
   const Entry x = s.x;
   const int64_t off = s.u1 - 1 - s.base;
-  const int item = s.u0 == s.u1 ? 0 : int(off / x.key_tiles);
-  const int64_t begin = s.base + int64_t(item) * x.key_tiles, end = begin + x.key_tiles;
+  const int item = s.u0 == s.u1 ? 0 : int(off / item_units(x));
+  const int64_t end = s.base + int64_t(item + 1) * item_units(x), begin = end - x.key_tiles;   // its key tiles
   // Every CTA waits, also those without an item: the launch after this one
   // may count on the attention kernel's end.
   grid_wait();
-  if (s.u0 == s.u1 || begin < s.u0 || end <= s.u1) return;
+  if (s.u0 == s.u1 || begin < s.u0 || begin >= s.u1 || end <= s.u1) return;
   if (*reinterpret_cast<volatile int32_t*>(p.status) != 0) return;
   Segments<R, KT> seg;
   seg.e = s.e;

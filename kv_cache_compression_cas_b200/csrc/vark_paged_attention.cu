@@ -37,6 +37,7 @@ struct AttnParams {
   int64_t N;
   int B, G, Hq, causal;
   int split;               // 1: equal shares of the key tiles; 0: a CTA per item
+  int item_cost;           // key tiles that an item counts for besides its own
   float scale_log2;        // log2(e) / sqrt(D)
   float* part_o;           // [kCtas][2][R][D]
   float* part_ml;          // [kCtas][2][R][2]
@@ -83,32 +84,38 @@ VARK_DEV Entry load_entry(const AttnParams& p, int e) {
   return x;
 }
 
-// Units of work (split): an item's key tiles, and one ahead of them for what
-// starting and finishing it costs (about a tile's time: without it the shares
-// with many short sequences ended last).  Not split: whole items.
-VARK_DEV int item_units(const Entry& x) { return x.key_tiles + 1; }
+// Units of work (split): an item's key tiles, and ahead of them item_cost for
+// what starting and finishing it takes (without them the shares with many short
+// sequences ended last).  Not split: whole items.
+VARK_DEV int item_units(const AttnParams& p, const Entry& x) { return x.key_tiles + p.item_cost; }
 VARK_DEV int64_t entry_units(const AttnParams& p, const Entry& x) {
-  return p.split ? int64_t(x.items) * item_units(x) : x.items;
+  return p.split ? int64_t(x.items) * item_units(p, x) : x.items;
 }
 
 struct Share {
-  int64_t total;           // units of the call
+  int ctas;                // shares of the call: extra of them have per + 1 units, the others per
+  int64_t per, extra;
   int64_t u0, u1;          // this CTA's units
-  int e;                   // entry of the unit asked for, its first unit, and itself
-  int64_t base;
-  Entry x;
+  struct Place {
+    int e;                 // an entry, its first unit, and itself
+    int64_t base;
+    Entry x;
+  };
+  Place first, last;       // where units u0 and u1 - 1 lie (last: on request)
+
+  VARK_DEV int64_t begin(int c) const { return per * c + min(int64_t(c), extra); }
+  VARK_DEV int holder(int64_t u) const {       // the share that unit u is in
+    const int64_t wide = extra * (per + 1);
+    return u < wide ? int(u / (per + 1)) : int(extra + (u - wide) / per);
+  }
 };
 
-VARK_DEV int64_t share_begin(int64_t total, int ctas, int c) { return total * c / ctas; }
-
-// Scan over the entries by the whole block: the share of CTA `cta`, and the
-// entry that holds its first (LAST = false) or last unit.
+// Scan over the entries by the whole block: the share of CTA `cta`, and where
+// its first unit (and with LAST its last one) lies.
 template <int R, int KT, int THREADS, bool LAST>
 VARK_DEV Share find_share(const AttnParams& p, int cta) {
   __shared__ int64_t warp_sum[THREADS / 32];
-  __shared__ int64_t found_base;
-  __shared__ int found_e;
-  __shared__ Entry found_x;
+  __shared__ Share::Place found[2];
   const int E = p.B * p.pg.table_heads;
   const int chunk = (E + THREADS - 1) / THREADS;
   const int e0 = min(E, int(threadIdx.x) * chunk), e1 = min(E, e0 + chunk);
@@ -128,38 +135,42 @@ VARK_DEV Share find_share(const AttnParams& p, int cta) {
   if (lane == 31) warp_sum[warp] = incl;
   __syncthreads();
   Share s;
-  s.total = 0;
-  int64_t before = 0;
+  int64_t before = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) {
     if (w < warp) before += warp_sum[w];
-    s.total += warp_sum[w];
+    total += warp_sum[w];
   }
-  const int ctas = int(p.split ? min(int64_t(kCtas), s.total) : s.total);
-  s.e = 0;
-  s.base = s.u0 = s.u1 = 0;
-  if (cta >= ctas) return s;     // the same for every thread
-  s.u0 = p.split ? share_begin(s.total, ctas, cta) : cta;
-  s.u1 = p.split ? share_begin(s.total, ctas, cta + 1) : cta + 1;
-  const int64_t want = LAST ? s.u1 - 1 : s.u0;
-  int64_t base = before + incl - sum;
-  if (want >= base && want < base + sum) {
+  s.ctas = int(p.split ? min(int64_t(kCtas), total) : total);
+  s.per = 1;
+  s.extra = 0;
+  if (p.split && total > kCtas) {
+    s.per = total < (int64_t(1) << 32) ? uint32_t(total) / uint32_t(kCtas) : total / kCtas;
+    s.extra = total - s.per * kCtas;
+  }
+  s.u0 = s.u1 = 0;
+  if (cta >= s.ctas) return s;   // the same for every thread
+  s.u0 = s.begin(cta);
+  s.u1 = s.begin(cta + 1);
+  const int64_t from = before + incl - sum;
+#pragma unroll
+  for (int k = 0; k < (LAST ? 2 : 1); ++k) {
+    const int64_t want = k ? s.u1 - 1 : s.u0;
+    if (want < from || want >= from + sum) continue;
+    int64_t base = from;
     for (int e = e0; e < e1; ++e) {
       if (chunk > 1) x = load_entry<R, KT>(p, e);     // (else it is the one just read)
       const int64_t w = entry_units(p, x);
       if (want < base + w) {
-        found_e = e;
-        found_base = base;
-        found_x = x;
+        found[k] = Share::Place{e, base, x};
         break;
       }
       base += w;
     }
   }
   __syncthreads();
-  s.e = found_e;
-  s.base = found_base;
-  s.x = found_x;
+  s.first = found[0];
+  if (LAST) s.last = found[1];
   return s;
 }
 
@@ -172,11 +183,11 @@ struct Segments {
   int h, tile, k0, k1;
 
   VARK_DEV void start(const AttnParams& p, const Share& s) {
-    e = s.e;
-    base = s.base;
+    e = s.first.e;
+    base = s.first.base;
     u = s.u0;
     u1 = s.u1;
-    x = s.x;
+    x = s.first.x;
   }
   VARK_DEV bool next(const AttnParams& p) {
     if (u >= u1) return false;
@@ -189,13 +200,14 @@ struct Segments {
     k0 = 0;
     k1 = x.key_tiles;
     if (p.split) {
-      item = int(off / item_units(x));
-      const int pos = int(off - int64_t(item) * item_units(x));
-      const int take = int(min(int64_t(item_units(x) - pos), u1 - u));
-      k0 = max(0, pos - 1);
-      k1 = pos + take - 1;
+      const int units = item_units(p, x);
+      item = off < (int64_t(1) << 32) ? int(uint32_t(off) / uint32_t(units)) : int(off / units);
+      const int pos = int(off - int64_t(item) * units);
+      const int take = int(min(int64_t(units - pos), u1 - u));
+      k0 = max(0, pos - p.item_cost);
+      k1 = pos + take - p.item_cost;
       u += take;
-      if (k1 == 0) return false;     // the share ends ahead of the item's first tile
+      if (k1 <= 0) return false;     // the share ends ahead of the item's first tile
     } else {
       ++u;
     }
@@ -778,10 +790,16 @@ struct RowSmem {
   static constexpr int kMisc = kBar + 2 * kSlots * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static_assert(kAlloc + 2048 <= kMaxSmem, "shared memory");
+  // Registers a thread: at launch, then of the loader's group and of the others.
+  // What is left of the SM's 65536 lets the join's CTA wait beside this one (two
+  // row tiles of 128 channels spill at 200, so there it follows instead).
+  static constexpr bool kWide = D * MT > 128;
+  static constexpr int kLaunchRegs = kWide ? 168 : 128, kLoadRegs = kWide ? 56 : 48, kWorkRegs = kWide ? 224 : 168;
+  static_assert(128 * kLoadRegs + 256 * kWorkRegs <= kRowThreads * kLaunchRegs, "registers");
 };
 
 template <int DT, int D, int MT>
-__global__ void __launch_bounds__(kRowThreads, 1)
+__global__ void __launch_bounds__(kRowThreads) __maxnreg__((RowSmem<D, MT>::kLaunchRegs))
 rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
             const __grid_constant__ AttnParams p) {
   using L = RowSmem<D, MT>;
@@ -816,11 +834,11 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   const Share share = find_share<L::kR, kTileKT, kRowThreads, false>(p, blockIdx.x);   // syncs the block
   if (share.u0 == share.u1) return;
   if (warp < 0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kLoadRegs) : "memory");
     if (warp == -4) load_tiles<D, L::kR, L>(p, share, tm_k, tm_v, sbase, abort_flag);
     return;
   }
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 224;" ::: "memory");
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kWorkRegs) : "memory");
   auto sync = [&]() { named_bar_sync(1, THREADS); };
 
   const int g = lane >> 2, t4 = lane & 3;
@@ -1095,109 +1113,123 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   }
 }
 
-// Joins the partial results of the item that starts in share c = blockIdx.x
-// and ends in a later one.  blockIdx.y: 64 of the tile's rows, taken 16 at a
-// time; where fewer rows exist, the threads of the others share the partials.
+// Joins partial results.  The CTAs whose shares hold a part of an item share its
+// rows: share c takes every n-th of them, n the number of parts (dealt on to the
+// gridDim.y CTAs of the share), and finds at most two such items, at its two
+// ends.  Threads that a few rows would
+// leave idle share the parts of a row.  (128 threads wait beside a running
+// rows kernel; one CTA per item took 5 us for 19 parts where this takes 2.)
+template <int R>
+struct JoinShape { static constexpr int kThreads = R == kTileR ? 256 : 128, kSplit = R == kTileR ? 4 : 1; };
+
 template <int DT, int D, int R, int KT>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(JoinShape<R>::kThreads) join_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int kThreads = JoinShape<R>::kThreads;
   constexpr int kChunk = D / 8;                     // threads of a row, 8 channels each
-  constexpr int kSlotsT = 256 / kChunk;             // (row, part) slots
-  __shared__ float red[kSlotsT][D + 4];
-  __shared__ float red_ml[kSlotsT][2];
+  constexpr int kRowSlots = kThreads / kChunk;  // (row, part) slots
+  __shared__ float red[kRowSlots][D + 4];
+  __shared__ float red_ml[kRowSlots][2];
   const int c = blockIdx.x;
   grid_release();
-  const Share s = find_share<R, KT, 256, true>(p, c);
-  const Entry x = s.x;
-  const int64_t off = s.u1 - 1 - s.base;
-  const int item = s.u0 == s.u1 ? 0 : int(off / item_units(x));
-  const int64_t end = s.base + int64_t(item + 1) * item_units(x), begin = end - x.key_tiles;   // its key tiles
+  const Share s = find_share<R, KT, kThreads, true>(p, c);
   // Every CTA waits, also those without an item: the launch after this one
   // may count on the attention kernel's end.
   grid_wait();
-  if (s.u0 == s.u1 || begin < s.u0 || begin >= s.u1 || end <= s.u1) return;
-  if (*reinterpret_cast<volatile int32_t*>(p.status) != 0) return;
-  Segments<R, KT> seg;
-  seg.e = s.e;
-  seg.x = x;
-  seg.h = p.pg.table_heads > 1 ? s.e % p.pg.heads : item / x.row_tiles;
-  seg.tile = item % x.row_tiles;
-  // the shares that hold a part: c, c + 1, ... while they start before the item ends
-  const int ctas = int(min(int64_t(kCtas), s.total));
-  int last = c + 1;
-  while (last + 1 < ctas && share_begin(s.total, ctas, last + 1) < end) ++last;
-  const int rows = min(R, x.n * p.G - seg.tile * R);
+  if (s.u0 == s.u1) return;
+  const int32_t status = *reinterpret_cast<volatile int32_t*>(p.status);
   const int d0 = (threadIdx.x % kChunk) * 8, slot = threadIdx.x / kChunk;
-  for (int r0 = blockIdx.y * 64; r0 < min(rows, int(blockIdx.y) * 64 + 64); r0 += kSlotsT) {
-    int width = 1;                                   // slots a part takes
-    while (width < min(kSlotsT, rows - r0)) width *= 2;
-    const int parts = kSlotsT / width, r = r0 + slot % width;
-    float top = -INFINITY, sum = 0.f, acc[8];
+  int64_t done = -1;                                // (one item may be at both ends)
+  for (int k = 0; k < 2; ++k) {
+    const Share::Place& at = k ? s.last : s.first;
+    const int units = item_units(p, at.x);
+    const int item = int(((k ? s.u1 - 1 : s.u0) - at.base) / units);
+    const int64_t end = at.base + int64_t(item + 1) * units, begin = end - at.x.key_tiles;   // its key tiles
+    if (begin >= s.u1 || (begin >= s.u0 && end <= s.u1) || begin == done) continue;           // none here, or all
+    done = begin;
+    const int c0 = s.holder(begin), n = s.holder(end - 1) - c0 + 1;                           // its parts' shares
+    if (n == 1) continue;
+    Segments<R, KT> seg;
+    seg.e = at.e;
+    seg.x = at.x;
+    seg.h = p.pg.table_heads > 1 ? at.e % p.pg.heads : item / at.x.row_tiles;
+    seg.tile = item % at.x.row_tiles;
+    const int rows = min(R, at.x.n * p.G - seg.tile * R);
+    const int r_first = c - c0 + int(blockIdx.y) * n, r_step = n * int(gridDim.y);
+    const int mine = (rows - r_first + r_step - 1) / r_step;
+    for (int r0 = 0; r0 < mine; r0 += kRowSlots) {
+      int width = 1;                                 // row slots of a part
+      while (width < min(kRowSlots, mine - r0)) width *= 2;
+      const int parts = kRowSlots / width;
+      const int i0 = r0 + slot % width, r = r_first + i0 * r_step;
+      float top = -INFINITY, sum = 0.f, acc[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-    if (r < rows) {
-      auto at = [&](int i) { return (int64_t(i) * 2 + (i == c ? 1 : 0)) * R + r; };
-      constexpr int kBatch = 3;                      // partials in flight a thread
-      for (int i0 = c + slot / width; i0 <= last; i0 += kBatch * parts) {
-        float2 v[kBatch];
-        float4 w[kBatch][2];
+      for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+      if (i0 < mine) {
+        constexpr int kBatch = 3;                    // partials in flight a thread
+        for (int q0 = slot / width; q0 < n; q0 += kBatch * parts) {
+          float2 v[kBatch];
+          float4 w[kBatch][2];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int i = i0 + k * parts;
-          v[k] = make_float2(-INFINITY, 0.f);
-          w[k][0] = w[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (i <= last) {
-            v[k] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + at(i) * 2));
-            w[k][0] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at(i) * D + d0));
-            w[k][1] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at(i) * D + d0 + 4));
+          for (int b = 0; b < kBatch; ++b) {
+            const int q = q0 + b * parts;
+            v[b] = make_float2(-INFINITY, 0.f);
+            w[b][0] = w[b][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (q < n) {
+              const int64_t from = (int64_t(c0 + q) * 2 + (q == 0 ? 1 : 0)) * R + r;
+              v[b] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + from * 2));
+              w[b][0] = __ldcg(reinterpret_cast<const float4*>(p.part_o + from * D + d0));
+              w[b][1] = __ldcg(reinterpret_cast<const float4*>(p.part_o + from * D + d0 + 4));
+            }
+          }
+          float big = top;
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) big = fmaxf(big, v[b].x);
+          const float ref = big == -INFINITY ? 0.f : big;
+          const float old = ex2_approx(top - ref);
+          top = big;
+          sum *= old;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] *= old;
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const float wgt = ex2_approx(v[b].x - ref);
+            sum = fmaf(v[b].y, wgt, sum);
+            const float z[8] = {w[b][0].x, w[b][0].y, w[b][0].z, w[b][0].w,
+                                w[b][1].x, w[b][1].y, w[b][1].z, w[b][1].w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = fmaf(z[e], wgt, acc[e]);
           }
         }
-        float big = top;
+      }
+      if (parts > 1) {
+        __syncthreads();
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) big = fmaxf(big, v[k].x);
-        const float ref = big == -INFINITY ? 0.f : big;
-        const float old = ex2_approx(top - ref);
-        top = big;
-        sum *= old;
+        for (int e = 0; e < 8; e += 4)
+          *reinterpret_cast<float4*>(&red[slot][d0 + e]) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+        if (d0 == 0) {
+          red_ml[slot][0] = top;
+          red_ml[slot][1] = sum;
+        }
+        __syncthreads();
+        if (slot < width) {
+          float big = top;
+          for (int q = 1; q < parts; ++q) big = fmaxf(big, red_ml[slot + q * width][0]);
+          const float ref = big == -INFINITY ? 0.f : big;
+          const float own = ex2_approx(top - ref);
+          top = big;
+          sum *= own;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] *= old;
+          for (int e = 0; e < 8; ++e) acc[e] *= own;
+          for (int q = 1; q < parts; ++q) {
+            const float wgt = ex2_approx(red_ml[slot + q * width][0] - ref);
+            sum = fmaf(red_ml[slot + q * width][1], wgt, sum);
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const float wgt = ex2_approx(v[k].x - ref);
-          sum = fmaf(v[k].y, wgt, sum);
-          const float z[8] = {w[k][0].x, w[k][0].y, w[k][0].z, w[k][0].w, w[k][1].x, w[k][1].y, w[k][1].z, w[k][1].w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) acc[e] = fmaf(z[e], wgt, acc[e]);
+            for (int e = 0; e < 8; ++e) acc[e] = fmaf(red[slot + q * width][d0 + e], wgt, acc[e]);
+          }
         }
       }
+      if (slot < width && i0 < mine && status == 0) store_row8<DT>(p, row_at(p, seg, r), d0, acc, top, sum);
     }
-    if (parts > 1) {
-      __syncthreads();
-#pragma unroll
-      for (int e = 0; e < 8; e += 4)
-        *reinterpret_cast<float4*>(&red[slot][d0 + e]) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
-      if (d0 == 0) {
-        red_ml[slot][0] = top;
-        red_ml[slot][1] = sum;
-      }
-      __syncthreads();
-      if (slot < width) {
-        float big = top;
-        for (int q = 1; q < parts; ++q) big = fmaxf(big, red_ml[slot + q * width][0]);
-        const float ref = big == -INFINITY ? 0.f : big;
-        const float own = ex2_approx(top - ref);
-        top = big;
-        sum *= own;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] *= own;
-        for (int q = 1; q < parts; ++q) {
-          const float wgt = ex2_approx(red_ml[slot + q * width][0] - ref);
-          sum = fmaf(red_ml[slot + q * width][1], wgt, sum);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) acc[e] = fmaf(red[slot + q * width][d0 + e], wgt, acc[e]);
-        }
-      }
-    }
-    if (slot < width && r < rows) store_row8<DT>(p, row_at(p, seg, r), d0, acc, top, sum);
   }
 }
 
@@ -1268,7 +1300,8 @@ static int launch_tiles(const CUtensorMap& k, const CUtensorMap& v, const AttnPa
   int rc = allow_smem(tiles_kernel<DT, D>, smem, &done);
   if (!rc) rc = launch_early(tiles_kernel<DT, D>, dim3(unsigned(grid)), kTileThreads, smem, st, k, v, p);
   if (rc || !p.split) return rc;
-  return launch_early(join_kernel<DT, D, kTileR, kTileKT>, dim3(kCtas, kTileR / 64), 256, 0, st, p);
+  using J = JoinShape<kTileR>;
+  return launch_early(join_kernel<DT, D, kTileR, kTileKT>, dim3(kCtas, J::kSplit), J::kThreads, 0, st, p);
 }
 
 template <int DT, int D, int MT>
@@ -1278,7 +1311,7 @@ static int launch_rows(const CUtensorMap& k, const CUtensorMap& v, const AttnPar
   int rc = allow_smem(rows_kernel<DT, D, MT>, smem, &done);
   if (!rc) rc = launch_early(rows_kernel<DT, D, MT>, dim3(kCtas), kRowThreads, smem, st, k, v, p);
   if (rc) return rc;
-  return launch_early(join_kernel<DT, D, 16 * MT, kTileKT>, dim3(kCtas), 256, 0, st, p);
+  return launch_early(join_kernel<DT, D, 16 * MT, kTileKT>, dim3(kCtas), JoinShape<16 * MT>::kThreads, 0, st, p);
 }
 
 template <int DT>
@@ -1359,6 +1392,7 @@ extern "C" int vark_paged_attention(int dtype, const uint16_t* q, const int64_t*
   const Variant var = choose(n_tokens, B, Hq, Hkv);
   if (var.items > INT32_MAX) return VARK_E_SHAPE;
   p.split = var.split;
+  p.item_cost = var.rows < kTileR && D == 64 ? 3 : 1;    // 2300-4000 cycles; a tile takes 2400 (D = 64: 1400)
   p.part_ml = static_cast<float*>(workspace);
   p.part_o = p.part_ml + int64_t(kCtas) * 2 * var.rows * 2;
   p.status = dev_status;

@@ -9,6 +9,7 @@ the stream.  A missing library raises at first use; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -603,7 +604,12 @@ def vark_pruned_attention_int3(q, kq, vq, k_scale, v_scale, kc_rows: int, k_dens
 
 
 # ------------------------------------------------------------------ paged cache
-_I64x2, _I64x3 = _I64 * 2, _I64 * 3
+@functools.lru_cache(maxsize=4096)
+def _i64_array(values):
+    """A C array of int64 that is only read (strides repeat from call to call,
+    and building one takes longer than finding it)."""
+    return (_I64 * len(values))(*values)
+
 
 
 def _paged_dtype(t, name):
@@ -740,10 +746,10 @@ def vark_qk_norm_rope(q, k, q_out, k_out, norm: int, q_weight, k_weight, eps: fl
         (k, "k", dtype, k_shape, 1), (k_out, "k_out", dtype, k_shape, 2), (k_weight, "k_weight", f32, (D,), 0),
         (rope, "rope", f32, rope_shape, 0), (positions, "positions", i32, (B, T), 0), _status_spec(dev_status, i32)))
     _check(_call_on(x.get_device(), stream, _load().vark_qk_norm_rope, dt,
-                    pq, None if q is None else _I64x3(*q.stride()[:3]),
-                    pqo, None if q is None else _I64x3(*q_out.stride()[:3]), Hq,
-                    pk, None if k is None else _I64x3(*k.stride()[:3]),
-                    pko, None if k is None else _I64x3(*k_out.stride()[:3]), Hk,
+                    pq, None if q is None else _i64_array(q.stride()),
+                    pqo, None if q is None else _i64_array(q_out.stride()), Hq,
+                    pk, None if k is None else _i64_array(k.stride()),
+                    pko, None if k is None else _i64_array(k_out.stride()), Hk,
                     B, T, D, norm, pqw, pkw, eps, pr, rope_len, rope_dim, 1 if pairs else 0, pp, ps),
            "vark_qk_norm_rope")
 
@@ -790,7 +796,7 @@ def vark_paged_append(k, v, cu_tokens, k_pages, v_pages, page_table, cache_len, 
               _status_spec(dev_status, torch.int32)]
     dev = k.get_device()
     kp, vp, tp, lp, cp, pk, pv, pw, pr, pp, ps = _pointers(dev, specs)
-    _check(_call_on(dev, stream, _load().vark_paged_append, dt, pk, _I64x2(*k.stride()[:2]), pv, _I64x2(*v.stride()[:2]), n, B,
+    _check(_call_on(dev, stream, _load().vark_paged_append, dt, pk, _i64_array(k.stride()), pv, _i64_array(v.stride()), n, B,
                     H, D, cp, kp, vp, n_pages, page_size, tp, max_pages, lp, head_pages, norm, pw, eps, pr, rope_len,
                     rope_dim, 1 if pairs else 0, pp, ps), "vark_paged_append")
 
@@ -824,6 +830,6 @@ def vark_paged_attention(q, cu_tokens, k_pages, v_pages, page_table, cache_len, 
               _status_spec(dev_status, torch.int32)]
     dev = q.get_device()
     kp, vp, tp, lp, cp, pq, po, pt, pl, pw, ps = _pointers(dev, specs)
-    _check(_call_on(dev, stream, _load().vark_paged_attention, dt, pq, _I64x2(*q.stride()[:2]), n, B, Hq, H, D, cp, kp, vp,
+    _check(_call_on(dev, stream, _load().vark_paged_attention, dt, pq, _i64_array(q.stride()), n, B, Hq, H, D, cp, kp, vp,
                     n_pages, page_size, tp, max_pages, lp, head_pages, pt, 1 if causal else 0, po,
-                    _I64x2(*out.stride()[:2]), pl, pw, workspace.numel(), ps), "vark_paged_attention")
+                    _i64_array(out.stride()), pl, pw, workspace.numel(), ps), "vark_paged_attention")

@@ -1116,120 +1116,120 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
 // Joins partial results.  The CTAs whose shares hold a part of an item share its
 // rows: share c takes every n-th of them, n the number of parts (dealt on to the
 // gridDim.y CTAs of the share), and finds at most two such items, at its two
-// ends.  Threads that a few rows would
-// leave idle share the parts of a row.  (128 threads wait beside a running
-// rows kernel; one CTA per item took 5 us for 19 parts where this takes 2.)
+// ends: one for each half of its threads.  Threads that a few rows would leave
+// idle share the parts of a row.  (The CTA waits beside a running rows kernel,
+// in the registers that leaves.  One CTA per item took 5 us for 19 parts.)
 template <int R>
-struct JoinShape { static constexpr int kThreads = R == kTileR ? 256 : 128, kSplit = R == kTileR ? 4 : 1; };
+struct JoinShape { static constexpr int kHalf = 128, kSplit = R == kTileR ? 4 : 1; };
 
 template <int DT, int D, int R, int KT>
-__global__ void __launch_bounds__(JoinShape<R>::kThreads) join_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int kThreads = JoinShape<R>::kThreads;
+__global__ void __launch_bounds__(2 * JoinShape<R>::kHalf, 4) join_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int kHalf = JoinShape<R>::kHalf;
   constexpr int kChunk = D / 8;                     // threads of a row, 8 channels each
-  constexpr int kRowSlots = kThreads / kChunk;  // (row, part) slots
-  __shared__ float red[kRowSlots][D + 4];
-  __shared__ float red_ml[kRowSlots][2];
+  constexpr int kRowSlots = kHalf / kChunk;     // (row, part) slots
+  __shared__ __align__(16) float red_all[2][kRowSlots][D + 4];
+  __shared__ float red_ml_all[2][kRowSlots][2];
   const int c = blockIdx.x;
   grid_release();
-  const Share s = find_share<R, KT, kThreads, true>(p, c);
+  const Share s = find_share<R, KT, 2 * kHalf, true>(p, c);
   // Every CTA waits, also those without an item: the launch after this one
   // may count on the attention kernel's end.
   grid_wait();
   if (s.u0 == s.u1) return;
   const int32_t status = *reinterpret_cast<volatile int32_t*>(p.status);
-  const int d0 = (threadIdx.x % kChunk) * 8, slot = threadIdx.x / kChunk;
-  int64_t done = -1;                                // (one item may be at both ends)
-  for (int k = 0; k < 2; ++k) {
-    const Share::Place& at = k ? s.last : s.first;
-    const int units = item_units(p, at.x);
-    const int item = int(((k ? s.u1 - 1 : s.u0) - at.base) / units);
-    const int64_t end = at.base + int64_t(item + 1) * units, begin = end - at.x.key_tiles;   // its key tiles
-    if (begin >= s.u1 || (begin >= s.u0 && end <= s.u1) || begin == done) continue;           // none here, or all
-    done = begin;
-    const int c0 = s.holder(begin), n = s.holder(end - 1) - c0 + 1;                           // its parts' shares
-    if (n == 1) continue;
-    Segments<R, KT> seg;
-    seg.e = at.e;
-    seg.x = at.x;
-    seg.h = p.pg.table_heads > 1 ? at.e % p.pg.heads : item / at.x.row_tiles;
-    seg.tile = item % at.x.row_tiles;
-    const int rows = min(R, at.x.n * p.G - seg.tile * R);
-    const int r_first = c - c0 + int(blockIdx.y) * n, r_step = n * int(gridDim.y);
-    const int mine = (rows - r_first + r_step - 1) / r_step;
-    for (int r0 = 0; r0 < mine; r0 += kRowSlots) {
-      int width = 1;                                 // row slots of a part
-      while (width < min(kRowSlots, mine - r0)) width *= 2;
-      const int parts = kRowSlots / width;
-      const int i0 = r0 + slot % width, r = r_first + i0 * r_step;
-      float top = -INFINITY, sum = 0.f, acc[8];
+  const int k = threadIdx.x / kHalf, tid = threadIdx.x % kHalf;
+  auto red = red_all[k];
+  auto red_ml = red_ml_all[k];
+  const int d0 = (tid % kChunk) * 8, slot = tid / kChunk;
+  const Share::Place& at = k ? s.last : s.first;
+  const int units = item_units(p, at.x);
+  const int item = int(((k ? s.u1 - 1 : s.u0) - at.base) / units);
+  const int64_t end = at.base + int64_t(item + 1) * units, begin = end - at.x.key_tiles;   // its key tiles
+  if (begin >= s.u1 || (begin >= s.u0 && end <= s.u1)) return;        // none of them here, or all
+  if (k == 1 && s.u0 >= end - units) return;                           // the first half's item too
+  const int c0 = s.holder(begin), n = s.holder(end - 1) - c0 + 1;                           // its parts' shares
+  if (n == 1) return;
+  Segments<R, KT> seg;
+  seg.e = at.e;
+  seg.x = at.x;
+  seg.h = p.pg.table_heads > 1 ? at.e % p.pg.heads : item / at.x.row_tiles;
+  seg.tile = item % at.x.row_tiles;
+  const int rows = min(R, at.x.n * p.G - seg.tile * R);
+  const int r_first = c - c0 + int(blockIdx.y) * n, r_step = n * int(gridDim.y);
+  const int mine = (rows - r_first + r_step - 1) / r_step;
+  for (int r0 = 0; r0 < mine; r0 += kRowSlots) {
+    int width = 1;                                 // row slots of a part
+    while (width < min(kRowSlots, mine - r0)) width *= 2;
+    const int parts = kRowSlots / width;
+    const int i0 = r0 + slot % width, r = r_first + i0 * r_step;
+    float top = -INFINITY, sum = 0.f, acc[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-      if (i0 < mine) {
-        constexpr int kBatch = 3;                    // partials in flight a thread
-        for (int q0 = slot / width; q0 < n; q0 += kBatch * parts) {
-          float2 v[kBatch];
-          float4 w[kBatch][2];
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    if (i0 < mine) {
+      constexpr int kBatch = 2;                    // partials in flight a thread
+      for (int q0 = slot / width; q0 < n; q0 += kBatch * parts) {
+        float2 v[kBatch];
+        float4 w[kBatch][2];
 #pragma unroll
-          for (int b = 0; b < kBatch; ++b) {
-            const int q = q0 + b * parts;
-            v[b] = make_float2(-INFINITY, 0.f);
-            w[b][0] = w[b][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (q < n) {
-              const int64_t from = (int64_t(c0 + q) * 2 + (q == 0 ? 1 : 0)) * R + r;
-              v[b] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + from * 2));
-              w[b][0] = __ldcg(reinterpret_cast<const float4*>(p.part_o + from * D + d0));
-              w[b][1] = __ldcg(reinterpret_cast<const float4*>(p.part_o + from * D + d0 + 4));
-            }
+        for (int b = 0; b < kBatch; ++b) {
+          const int q = q0 + b * parts;
+          v[b] = make_float2(-INFINITY, 0.f);
+          w[b][0] = w[b][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (q < n) {
+            const int64_t from = (int64_t(c0 + q) * 2 + (q == 0 ? 1 : 0)) * R + r;
+            v[b] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + from * 2));
+            w[b][0] = __ldcg(reinterpret_cast<const float4*>(p.part_o + from * D + d0));
+            w[b][1] = __ldcg(reinterpret_cast<const float4*>(p.part_o + from * D + d0 + 4));
           }
-          float big = top;
+        }
+        float big = top;
 #pragma unroll
-          for (int b = 0; b < kBatch; ++b) big = fmaxf(big, v[b].x);
-          const float ref = big == -INFINITY ? 0.f : big;
-          const float old = ex2_approx(top - ref);
-          top = big;
-          sum *= old;
+        for (int b = 0; b < kBatch; ++b) big = fmaxf(big, v[b].x);
+        const float ref = big == -INFINITY ? 0.f : big;
+        const float old = ex2_approx(top - ref);
+        top = big;
+        sum *= old;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc[e] *= old;
+        for (int e = 0; e < 8; ++e) acc[e] *= old;
 #pragma unroll
-          for (int b = 0; b < kBatch; ++b) {
-            const float wgt = ex2_approx(v[b].x - ref);
-            sum = fmaf(v[b].y, wgt, sum);
-            const float z[8] = {w[b][0].x, w[b][0].y, w[b][0].z, w[b][0].w,
-                                w[b][1].x, w[b][1].y, w[b][1].z, w[b][1].w};
+        for (int b = 0; b < kBatch; ++b) {
+          const float wgt = ex2_approx(v[b].x - ref);
+          sum = fmaf(v[b].y, wgt, sum);
+          const float z[8] = {w[b][0].x, w[b][0].y, w[b][0].z, w[b][0].w,
+                              w[b][1].x, w[b][1].y, w[b][1].z, w[b][1].w};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] = fmaf(z[e], wgt, acc[e]);
-          }
+          for (int e = 0; e < 8; ++e) acc[e] = fmaf(z[e], wgt, acc[e]);
         }
       }
-      if (parts > 1) {
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < 8; e += 4)
-          *reinterpret_cast<float4*>(&red[slot][d0 + e]) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
-        if (d0 == 0) {
-          red_ml[slot][0] = top;
-          red_ml[slot][1] = sum;
-        }
-        __syncthreads();
-        if (slot < width) {
-          float big = top;
-          for (int q = 1; q < parts; ++q) big = fmaxf(big, red_ml[slot + q * width][0]);
-          const float ref = big == -INFINITY ? 0.f : big;
-          const float own = ex2_approx(top - ref);
-          top = big;
-          sum *= own;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) acc[e] *= own;
-          for (int q = 1; q < parts; ++q) {
-            const float wgt = ex2_approx(red_ml[slot + q * width][0] - ref);
-            sum = fmaf(red_ml[slot + q * width][1], wgt, sum);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] = fmaf(red[slot + q * width][d0 + e], wgt, acc[e]);
-          }
-        }
-      }
-      if (slot < width && i0 < mine && status == 0) store_row8<DT>(p, row_at(p, seg, r), d0, acc, top, sum);
     }
+    if (parts > 1) {
+      named_bar_sync(1 + k, kHalf);
+#pragma unroll
+      for (int e = 0; e < 8; e += 4)
+        *reinterpret_cast<float4*>(&red[slot][d0 + e]) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+      if (d0 == 0) {
+        red_ml[slot][0] = top;
+        red_ml[slot][1] = sum;
+      }
+      named_bar_sync(1 + k, kHalf);
+      if (slot < width) {
+        float big = top;
+        for (int q = 1; q < parts; ++q) big = fmaxf(big, red_ml[slot + q * width][0]);
+        const float ref = big == -INFINITY ? 0.f : big;
+        const float own = ex2_approx(top - ref);
+        top = big;
+        sum *= own;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] *= own;
+        for (int q = 1; q < parts; ++q) {
+          const float wgt = ex2_approx(red_ml[slot + q * width][0] - ref);
+          sum = fmaf(red_ml[slot + q * width][1], wgt, sum);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] = fmaf(red[slot + q * width][d0 + e], wgt, acc[e]);
+        }
+      }
+    }
+    if (slot < width && i0 < mine && status == 0) store_row8<DT>(p, row_at(p, seg, r), d0, acc, top, sum);
   }
 }
 
@@ -1301,7 +1301,7 @@ static int launch_tiles(const CUtensorMap& k, const CUtensorMap& v, const AttnPa
   if (!rc) rc = launch_early(tiles_kernel<DT, D>, dim3(unsigned(grid)), kTileThreads, smem, st, k, v, p);
   if (rc || !p.split) return rc;
   using J = JoinShape<kTileR>;
-  return launch_early(join_kernel<DT, D, kTileR, kTileKT>, dim3(kCtas, J::kSplit), J::kThreads, 0, st, p);
+  return launch_early(join_kernel<DT, D, kTileR, kTileKT>, dim3(kCtas, J::kSplit), 2 * J::kHalf, 0, st, p);
 }
 
 template <int DT, int D, int MT>
@@ -1311,7 +1311,7 @@ static int launch_rows(const CUtensorMap& k, const CUtensorMap& v, const AttnPar
   int rc = allow_smem(rows_kernel<DT, D, MT>, smem, &done);
   if (!rc) rc = launch_early(rows_kernel<DT, D, MT>, dim3(kCtas), kRowThreads, smem, st, k, v, p);
   if (rc) return rc;
-  return launch_early(join_kernel<DT, D, 16 * MT, kTileKT>, dim3(kCtas), JoinShape<16 * MT>::kThreads, 0, st, p);
+  return launch_early(join_kernel<DT, D, 16 * MT, kTileKT>, dim3(kCtas), 2 * JoinShape<16 * MT>::kHalf, 0, st, p);
 }
 
 template <int DT>

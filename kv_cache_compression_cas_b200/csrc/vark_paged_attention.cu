@@ -36,7 +36,6 @@ struct AttnParams {
   const float* tau;        // [Hq] or null
   int64_t N;
   int B, G, Hq, causal;
-  int split;               // 1: equal shares of the key tiles; 0: a CTA per item
   int item_cost;           // key tiles that an item counts for besides its own
   float scale_log2;        // log2(e) / sqrt(D)
   float* part_o;           // [kCtas][2][R][D]
@@ -55,12 +54,43 @@ VARK_DEV void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ------------------------------------------------------------------ the plan
 // An entry is one row of the length table: a sequence (shared pages, all kv
-// heads) or a (sequence, head).
+// heads) or a (sequence, head).  Its items, head after head and row tile after
+// row tile, weigh what they cost, in sixteenths of a key: item_cost tiles for
+// starting and finishing one, and the keys its rows see -- which under a causal
+// mask grow by the tokens of a tile from one row tile to the next, so the
+// weights and their sums have a closed form.  (Equal weights left causal
+// prompts with shares of 0.6 to 1.5 times the mean work.)
+constexpr int kUnit = 16;
+// a / b of non-negative numbers, in 32 bits where they allow it (64 take ten
+// times as long).
+VARK_DEV int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
+}
 struct Entry {
   int first, n;            // first token, tokens
   int len;                 // cache rows
-  int row_tiles, key_tiles;
-  int items;               // kv heads of the entry * row_tiles
+  int row_tiles, heads;    // row tiles of a head, kv heads of the entry
+  int slope;               // weight of row tile t: weight0 + t * slope
+  int64_t weight0;
+
+  VARK_DEV int64_t sum(int t) const { return t * weight0 + int64_t(slope) * t * (t - 1) / 2; }   // of tiles 0 .. t-1
+  VARK_DEV int64_t head_units() const { return sum(row_tiles); }
+  VARK_DEV int64_t units() const { return heads * head_units(); }
+  // The row tile that holds unit `off` of a head.
+  VARK_DEV int tile_of(int64_t off) const {
+    int t;
+    if (row_tiles == 1) return 0;
+    if (slope == 0) {
+      t = int(quotient(off, weight0));
+    } else {
+      const double lin = double(weight0) - 0.5 * slope;
+      t = int((sqrt(lin * lin + 2.0 * slope * double(off)) - lin) / slope);
+    }
+    t = max(0, min(row_tiles - 1, t));
+    while (t > 0 && sum(t) > off) --t;
+    while (t + 1 < row_tiles && sum(t + 1) <= off) ++t;
+    return t;
+  }
 };
 
 // Lengths and token offsets that do not fit the arguments leave the entry
@@ -79,18 +109,25 @@ VARK_DEV Entry load_entry(const AttnParams& p, int e) {
     x.n = end - x.first;
   }
   x.row_tiles = (x.n * p.G + R - 1) / R;
-  x.key_tiles = max(1, (x.len + KT - 1) / KT);
-  x.items = x.row_tiles * (p.pg.table_heads > 1 ? 1 : p.pg.heads);
+  x.heads = p.pg.table_heads > 1 ? 1 : p.pg.heads;
+  x.slope = p.causal && x.row_tiles > 1 ? R * kUnit / p.G : 0;
+  const int seen0 = x.slope ? min(x.len, max(0, x.len - x.n) + R / p.G) : x.len;     // by the first row tile
+  x.weight0 = int64_t(kUnit) * (int64_t(p.item_cost) * KT + seen0);
   return x;
 }
 
-// Units of work (split): an item's key tiles, and ahead of them item_cost for
-// what starting and finishing it takes (without them the shares with many short
-// sequences ended last).  Not split: whole items.
-VARK_DEV int item_units(const AttnParams& p, const Entry& x) { return x.key_tiles + p.item_cost; }
-VARK_DEV int64_t entry_units(const AttnParams& p, const Entry& x) {
-  return p.split ? int64_t(x.items) * item_units(p, x) : x.items;
-}
+// Where an item's key tiles lie in its units [from, to): after its fixed cost;
+// the tile that unit u has come to (the last unit is the end of all tiles).
+struct ItemPlace {
+  int64_t from, to;
+  int key_tiles;
+  template <int KT>
+  VARK_DEV int tile_at(const AttnParams& p, int64_t u) const {
+    if (u >= to) return key_tiles;
+    const int64_t k = (u - from) / (kUnit * KT) - p.item_cost;
+    return int(max(int64_t(0), min(int64_t(key_tiles), k)));
+  }
+};
 
 struct Share {
   int ctas;                // shares of the call: extra of them have per + 1 units, the others per
@@ -106,7 +143,7 @@ struct Share {
   VARK_DEV int64_t begin(int c) const { return per * c + min(int64_t(c), extra); }
   VARK_DEV int holder(int64_t u) const {       // the share that unit u is in
     const int64_t wide = extra * (per + 1);
-    return u < wide ? int(u / (per + 1)) : int(extra + (u - wide) / per);
+    return u < wide ? int(quotient(u, per + 1)) : int(extra + quotient(u - wide, per));
   }
 };
 
@@ -120,10 +157,10 @@ VARK_DEV Share find_share(const AttnParams& p, int cta) {
   const int chunk = (E + THREADS - 1) / THREADS;
   const int e0 = min(E, int(threadIdx.x) * chunk), e1 = min(E, e0 + chunk);
   int64_t sum = 0;
-  Entry x = {0, 0, 0, 0, 0, 0};
+  Entry x = {};
   for (int e = e0; e < e1; ++e) {
     x = load_entry<R, KT>(p, e);
-    sum += entry_units(p, x);
+    sum += x.units();
   }
   int64_t incl = sum;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -141,11 +178,11 @@ VARK_DEV Share find_share(const AttnParams& p, int cta) {
     if (w < warp) before += warp_sum[w];
     total += warp_sum[w];
   }
-  s.ctas = int(p.split ? min(int64_t(kCtas), total) : total);
+  s.ctas = int(min(int64_t(kCtas), total));
   s.per = 1;
   s.extra = 0;
-  if (p.split && total > kCtas) {
-    s.per = total < (int64_t(1) << 32) ? uint32_t(total) / uint32_t(kCtas) : total / kCtas;
+  if (total > kCtas) {
+    s.per = quotient(total, kCtas);
     s.extra = total - s.per * kCtas;
   }
   s.u0 = s.u1 = 0;
@@ -160,7 +197,7 @@ VARK_DEV Share find_share(const AttnParams& p, int cta) {
     int64_t base = from;
     for (int e = e0; e < e1; ++e) {
       if (chunk > 1) x = load_entry<R, KT>(p, e);     // (else it is the one just read)
-      const int64_t w = entry_units(p, x);
+      const int64_t w = x.units();
       if (want < base + w) {
         found[k] = Share::Place{e, base, x};
         break;
@@ -174,48 +211,60 @@ VARK_DEV Share find_share(const AttnParams& p, int cta) {
   return s;
 }
 
-// A run of key tiles [k0, k1) of one item.
+// The runs of key tiles [k0, k1) of a share, item after item.
 template <int R, int KT>
 struct Segments {
-  int e;
-  int64_t base, u, u1;     // first unit of entry e, next unit, end of the share
   Entry x;
-  int h, tile, k0, k1;
+  int e, i;                // entry, head within it
+  int64_t u, u1;           // next unit, end of the share
+  ItemPlace at;            // the item of the segment
+  int tile, h, k0, k1;
 
   VARK_DEV void start(const AttnParams& p, const Share& s) {
     e = s.first.e;
-    base = s.first.base;
+    x = s.first.x;
     u = s.u0;
     u1 = s.u1;
-    x = s.first.x;
+    find(p, s.first.base, u);
   }
   VARK_DEV bool next(const AttnParams& p) {
-    if (u >= u1) return false;
-    while (u >= base + entry_units(p, x)) {
-      base += entry_units(p, x);
-      x = load_entry<R, KT>(p, ++e);
+    while (u < u1) {
+      if (u == at.to) step(p);
+      const int64_t stop = min(at.to, u1);
+      k0 = at.tile_at<KT>(p, u);
+      k1 = at.tile_at<KT>(p, stop);
+      u = stop;
+      if (k0 < k1) return true;      // (else a share's end fell into the item's fixed cost)
     }
-    const int64_t off = u - base;
-    int item = int(off);
-    k0 = 0;
-    k1 = x.key_tiles;
-    if (p.split) {
-      const int units = item_units(p, x);
-      item = off < (int64_t(1) << 32) ? int(uint32_t(off) / uint32_t(units)) : int(off / units);
-      const int pos = int(off - int64_t(item) * units);
-      const int take = int(min(int64_t(units - pos), u1 - u));
-      k0 = max(0, pos - p.item_cost);
-      k1 = pos + take - p.item_cost;
-      u += take;
-      if (k1 <= 0) return false;     // the share ends ahead of the item's first tile
-    } else {
-      ++u;
+    return false;
+  }
+  VARK_DEV bool whole() const { return k0 == 0 && k1 == at.key_tiles; }
+  // The item of entry e, whose first unit is `base`, that holds unit v.
+  VARK_DEV void find(const AttnParams& p, int64_t base, int64_t v) {
+    const int64_t per_head = x.head_units();
+    int64_t off = v - base;
+    i = x.heads == 1 ? 0 : int(quotient(off, per_head));
+    off -= i * per_head;
+    tile = x.tile_of(off);
+    at.from = base + i * per_head + x.sum(tile);
+    place(p);
+  }
+  VARK_DEV void step(const AttnParams& p) {
+    at.from = at.to;
+    if (++tile == x.row_tiles) {
+      tile = 0;
+      if (++i == x.heads) {
+        i = 0;
+        do x = load_entry<R, KT>(p, ++e);
+        while (x.row_tiles == 0);
+      }
     }
-    h = p.pg.table_heads > 1 ? e % p.pg.heads : item / x.row_tiles;
-    tile = item % x.row_tiles;
-    // a sequence's last rows see the most keys under a causal mask: first
-    if (!p.split) tile = x.row_tiles - 1 - tile;
-    return true;
+    place(p);
+  }
+  VARK_DEV void place(const AttnParams& p) {
+    h = p.pg.table_heads > 1 ? e % p.pg.heads : i;
+    at.to = at.from + x.weight0 + int64_t(tile) * x.slope;
+    at.key_tiles = max(1, (limit(p) + KT - 1) / KT);
   }
   // Keys that some row of the tile sees.
   VARK_DEV int limit(const AttnParams& p) const {
@@ -259,7 +308,8 @@ VARK_DEV void store_row8(const AttnParams& p, const RowAt& a, int d0, const floa
 // CTA works on 256 rows as two tiles of 128 (A, B) that see the same key tiles,
 // so every key tile is loaded once for both.  Warp 0 loads key and value
 // tiles of 128 rows by TMA, one box per page, into one ring of slots (K_0, V_0,
-// K_1, V_1, ...); warp 1 issues the MMAs PV_A(j-1), S_A(j), PV_B(j-1), S_B(j),
+// K_1, V_1, ...); warps 2 and 3 bring the queries of A and B, a segment ahead of
+// their use; warp 1 issues the MMAs PV_A(j-1), S_A(j), PV_B(j-1), S_B(j),
 // so the softmax of one tile overlaps the products of the other; warps 4-7 and
 // 8-11 are the softmax of A and B, one thread per row (TMEM lane).  S is read
 // from tensor memory, and P written back over its first 64 columns in the type
@@ -312,17 +362,19 @@ template <int D>
 struct TileSmem {
   static constexpr int kPanel = 128 * 128;            // 128 rows x 64 channels
   static constexpr int kTile = (D / 64) * kPanel;
-  static constexpr int kSlots = D == 128 ? 5 : 8;
+  static constexpr int kSlots = D == 128 ? 4 : 8;
   static constexpr int kQ = 0;                        // [2 tiles]
   static constexpr int kRing = kQ + 2 * kTile;        // [kSlots]
-  static constexpr int kBar = kRing + kSlots * kTile;
+  static constexpr int kStage = kRing + kSlots * kTile;   // [8 softmax warps] 32 rows of 128 bytes on their way out
+  static constexpr int kStageBytes = 32 * 128;
+  static constexpr int kBar = kStage + 8 * kStageBytes;
   static constexpr int kFull = 0, kEmpty = kSlots;    // barrier indices
-  static constexpr int kQFull = 2 * kSlots, kS = kQFull + 2, kP = kS + 2, kO = kP + 2, kDrain = kO + 2;
-  static constexpr int kNumBars = kDrain + 1;
+  static constexpr int kQFull = 2 * kSlots, kQFree = kQFull + 2, kS = kQFree + 2, kP = kS + 2, kO = kP + 2;
+  static constexpr int kDrain = kO + 2, kNumBars = kDrain + 1;
   static constexpr int kMisc = kBar + kNumBars * 8;   // tmem base, abort flag
-  static constexpr int kSeg = kMisc + 16;             // [8 softmax warps] segment (kept out of their registers)
-  static constexpr int kSegBytes = 96;
-  static constexpr int kAlloc = kSeg + 8 * kSegBytes + 1024;
+  static constexpr int kSeg = kMisc + 16;             // [warps 1-3, 8 softmax warps] segment, out of their registers
+  static constexpr int kSegBytes = 112;
+  static constexpr int kAlloc = kSeg + 11 * kSegBytes;
   static_assert(kAlloc + 1024 <= kMaxSmem, "shared memory");
 };
 
@@ -407,6 +459,33 @@ VARK_DEV void load_tiles(const AttnParams& p, const Share& share, const CUtensor
     mbar_wait(bar(L::kFull + i % L::kSlots), (i / L::kSlots) & 1, &no_abort, nullptr);
 }
 
+VARK_DEV uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// 16 bytes to shared memory without a register, zeros for `bytes` = 0.
+VARK_DEV void copy_async16(uint32_t dst, const uint16_t* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+VARK_DEV void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Steps a warp's segment in shared memory.
+template <int R, int KT>
+VARK_DEV bool next_segment(const AttnParams& p, Segments<R, KT>& sg) {
+  __syncwarp();
+  Segments<R, KT> next = sg;          // every lane steps a copy in registers
+  const bool more = next.next(p);
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) sg = next;
+  __syncwarp();
+  return more;
+}
+
 template <int DT, int D>
 __global__ void __launch_bounds__(kTileThreads, 1)
 tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -414,9 +493,14 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
   using L = TileSmem<D>;
   using Seg = Segments<kTileR, kTileKT>;
   using Ring = RingAt<L::kSlots>;
+  static_assert(sizeof(Seg) <= L::kSegBytes && sizeof(Seg) % 8 == 0 && L::kSeg % 8 == 0, "segment");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* smem = smem_raw;
   const uint32_t sbase = smem_u32(smem);
+  if (sbase & 1023u) {      // (the swizzle counts on the alignment; there is no room to move the base)
+    record(p.status, VARK_E_CUDA);
+    return;
+  }
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   auto bar = [&](int i) { return sbase + L::kBar + 8u * uint32_t(i); };
@@ -432,7 +516,8 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
       mbar_init(bar(L::kEmpty + i), 1);
     }
     for (int x = 0; x < 2; ++x) {
-      mbar_init(bar(L::kQFull + x), 4);
+      mbar_init(bar(L::kQFull + x), 1);
+      mbar_init(bar(L::kQFree + x), 1);
       mbar_init(bar(L::kS + x), 1);
       mbar_init(bar(L::kP + x), 4);
       mbar_init(bar(L::kO + x), 1);
@@ -481,12 +566,12 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         for (int k = 0; k < 8; ++k)
           mma_ts(lead, tmem + 256 + x * D, tmem + x * 128 + k * 8, b + k * (2048 >> 4), idesc_o, k > 0 ? 1u : acc);
       };
-      Seg sg;
-      sg.start(p, share);
+      Seg& sg = *reinterpret_cast<Seg*>(smem + L::kSeg);
+      if (lane == 0) sg.start(p, share);
       Ring kr = {0, 0}, vr = {1, 0};
       int q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
       bool ok = true;
-      while (ok && sg.next(p)) {
+      while (ok && next_segment(p, sg)) {
         const int nt = seen_tiles(p, sg);
         const int n_act = sg.x.n * p.G - sg.tile * kTileR > 128 ? 2 : 1;
         for (int j = 0; ok && j <= nt && nt > 0; ++j) {
@@ -510,6 +595,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
             if (j < nt) {
               issue_s(x, kr.slot);
               commit(lead, bar(L::kS + x));
+              if (j == nt - 1) commit(lead, bar(L::kQFree + x));
             } else {
               commit(lead, bar(L::kO + x));
             }
@@ -529,6 +615,55 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
       commit(lead, bar(L::kDrain));
       volatile int no_abort = 0;
       mbar_wait(bar(L::kDrain), 0, &no_abort, nullptr);
+    } else {
+      // -------------------------------------------------------- queries
+      // Tile x's 128 rows, 128-byte swizzled, D / 8 lanes a row.  Under a
+      // negative temperature the query's sign is turned instead, so the
+      // largest score gives the largest logit; under 0 the query is 0.
+      constexpr int kRowLanes = D / 8, kRowsAt = 32 / kRowLanes;
+      const int x = warp - 2;
+      const uint32_t sq = sbase + L::kQ + x * L::kTile;
+      auto chunk_at = [&](int w, int c) { return sq + (c >> 3) * L::kPanel + w * 128 + (((c & 7) ^ (w & 7)) << 4); };
+      Seg& sg = *reinterpret_cast<Seg*>(smem + L::kSeg + (warp - 1) * L::kSegBytes);
+      if (lane == 0) sg.start(p, share);
+      int uses = 0;
+      bool ok = true;
+      while (ok && next_segment(p, sg)) {
+        if (seen_tiles(p, sg) == 0 || (x == 1 && sg.x.n * p.G - sg.tile * kTileR <= 128)) continue;
+        if (uses > 0) ok = __all_sync(0xffffffffu, wait(L::kQFree + x, (uses - 1) & 1));
+        if (!ok) break;
+        ++uses;
+        bool turned = false;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const RowAt row = row_at(p, sg, x * 128 + q * 32 + lane);
+          const float tau = p.tau != nullptr && row.token >= 0 ? p.tau[row.head] : 1.f;
+          const int64_t off = row.token < 0 || tau == 0.f ? -1 : row.token * p.qs[0] + row.head * p.qs[1];
+          turned |= tau < 0.f;
+#pragma unroll 4
+          for (int it = 0; it < 32 / kRowsAt; ++it) {
+            const int w = it * kRowsAt + lane / kRowLanes, c = lane % kRowLanes;
+            const int64_t from = __shfl_sync(0xffffffffu, off, w);
+            copy_async16(chunk_at(q * 32 + w, c), p.q + (from < 0 ? 0 : from) + c * 8, from < 0 ? 0 : 16);
+          }
+        }
+        copy_async_wait();
+        __syncwarp();
+        if (__any_sync(0xffffffffu, turned)) {
+          for (int q = 0; q < 4; ++q) {
+            const RowAt row = row_at(p, sg, x * 128 + q * 32 + lane);
+            if (row.token < 0 || !(p.tau[row.head] < 0.f)) continue;
+            for (int c = 0; c < kRowLanes; ++c) {
+              uint4 v = ld_shared_v4(chunk_at(q * 32 + lane, c));
+              v.x ^= 0x80008000u; v.y ^= 0x80008000u; v.z ^= 0x80008000u; v.w ^= 0x80008000u;
+              st_shared_v4(chunk_at(q * 32 + lane, c), v);
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kQFull + x));
+      }
     }
   } else {
     setmaxnreg_inc224();
@@ -541,44 +676,45 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     int s_phase = 0, o_phase = 0;
     Ring vr = {1, 0};
     bool ok = true;
-    static_assert(sizeof(Seg) <= L::kSegBytes, "segment");
-    Seg& sg = *reinterpret_cast<Seg*>(smem + L::kSeg + (warp - 4) * L::kSegBytes);
-    auto next_segment = [&]() {
-      __syncwarp();
-      const int more = __any_sync(0xffffffffu, lane == 0 && sg.next(p));
-      __syncwarp();
-      return more != 0;
-    };
+    Seg& sg = *reinterpret_cast<Seg*>(smem + L::kSeg + (warp - 1) * L::kSegBytes);
     if (lane == 0) sg.start(p, share);
-    while (ok && next_segment()) {
-      const int nt = seen_tiles(p, sg);
-      const bool active = x == 0 || sg.x.n * p.G - sg.tile * kTileR > 128;
-      if (!active) continue;      // (only tile B can be empty)
-      const RowAt row = row_at(p, sg, x * 128 + r);
-      float qk2 = p.scale_log2;
-      if (p.tau != nullptr && row.token >= 0) qk2 *= p.tau[row.head];
-      // Q to shared memory, 128-byte swizzled.  S_X of the last segment is
-      // complete, so its Q is free.  Under a negative temperature the query's
-      // sign is turned instead, so the largest score gives the largest logit.
-      if (nt > 0) {
-        const uint32_t flip = qk2 < 0.f ? 0x80008000u : 0u;
-        qk2 = fabsf(qk2);
-        const uint16_t* src = row.token < 0 ? nullptr : p.q + row.token * p.qs[0] + row.head * p.qs[1];
-        const uint32_t dst = sbase + L::kQ + x * L::kTile + r * 128;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          uint4 w = make_uint4(0u, 0u, 0u, 0u);
-          if (src != nullptr) w = *reinterpret_cast<const uint4*>(src + c * 8);
-          w.x ^= flip; w.y ^= flip; w.z ^= flip; w.w ^= flip;
-          st_shared_v4(dst + (c >> 3) * L::kPanel + (((c & 7) ^ (r & 7)) << 4), w);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::kQFull + x));
+    // This row's part of a segment; the next one's is found while the last
+    // products of the one before are still running.
+    struct Work {
+      RowAt row;
+      int nt, seen, held;    // key tiles; keys from the first tile on that the row sees, that the cache holds
+      int seen_min;          // over the warp's rows
+      float qk2;             // (the temperature's sign is in the query, as is a zero)
+      bool whole;
+      int slot;
+    } cur;
+    auto take = [&](Work& w) {
+      do {
+        if (!next_segment(p, sg)) return false;
+      } while (x == 1 && sg.x.n * p.G - sg.tile * kTileR <= 128);      // tile B may be empty
+      w.row = row_at(p, sg, x * 128 + r);
+      w.qk2 = p.scale_log2;
+      if (p.tau != nullptr && w.row.token >= 0) {
+        const float tau = p.tau[w.row.head];
+        w.qk2 = tau == 0.f ? 1.f : w.qk2 * fabsf(tau);
       }
+      w.nt = seen_tiles(p, sg);
+      // (a row that does not exist needs no mask: nothing reads what it makes)
+      w.seen = (w.row.token < 0 ? (1 << 30) : w.row.limit) - sg.k0 * kTileKT;
+      w.held = sg.x.len - sg.k0 * kTileKT;
+      w.seen_min = __reduce_min_sync(0xffffffffu, w.seen);
+      w.whole = sg.whole();
+      w.slot = (int(blockIdx.x) * 2 + (sg.k0 == 0 ? 1 : 0)) * kTileR + x * 128 + r;
+      return true;
+    };
+    bool more = take(cur);
+    while (more) {
+      const RowAt row = cur.row;
+      const int nt = cur.nt, slot = cur.slot;
+      const bool whole = cur.whole;
+      const float qk2 = cur.qk2;
       float m_used = -INFINITY, l_sum = 0.f;
-      int seen = row.limit - sg.k0 * kTileKT;           // columns of the tile that this row sees,
-      int held = sg.x.len - sg.k0 * kTileKT;            // and that the cache holds
+      int seen = cur.seen, held = cur.held, seen_min = cur.seen_min;
       for (int j = 0; j < nt; ++j) {
         ok = __all_sync(0xffffffffu, wait(L::kS + x, s_phase));
         if (!ok) break;
@@ -597,10 +733,9 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
             for (int i = 0; i < 32; ++i) sv[c * 32 + i] = __uint_as_float(v[c][i]);
           }
         }
-        const bool edge = __any_sync(0xffffffffu, seen < kTileKT);
-        if (edge) {
+        if (seen_min < kTileKT) {
 #pragma unroll
-          for (int c = 0; c < 128; ++c) sv[c] = c < seen ? sv[c] * qk2 : -INFINITY;
+          for (int c = 0; c < 128; ++c) sv[c] = c < seen ? sv[c] : -INFINITY;
         }
         float m0 = sv[0], m1 = sv[1], m2 = sv[2], m3 = sv[3];
 #pragma unroll
@@ -612,8 +747,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         }
         m0 = fmax3(m0, sv[124], sv[125]);
         m1 = fmax3(m1, sv[126], sv[127]);
-        const float mul = edge ? 1.f : qk2;
-        const float m_tile = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * mul;
+        const float m_tile = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * qk2;
         float f = 1.f;
         if (m_tile > m_used + kRescale || (m_used == -INFINITY && m_tile > -INFINITY)) {
           f = ex2_approx(m_used - m_tile);
@@ -621,7 +755,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
           l_sum *= f;
         }
         if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {   // O_X is stable: S_X(j) came after PV_X(j-1)
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t v[32];
             tmem_ld32(tO + c * 32, v);
@@ -634,7 +768,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         }
         const float shift = m_used == -INFINITY ? 0.f : -m_used;
 #pragma unroll
-        for (int c = 0; c < 128; c += 2) ffma2(sv[c], sv[c + 1], sv[c], sv[c + 1], mul, mul, shift, shift);
+        for (int c = 0; c < 128; c += 2) ffma2(sv[c], sv[c + 1], sv[c], sv[c + 1], qk2, qk2, shift, shift);
 #pragma unroll
         for (int c = 0; c < 128; ++c) sv[c] = ex2_approx(sv[c]);
 #pragma unroll
@@ -660,6 +794,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         }
         vr.skip(2);
         seen -= kTileKT;
+        seen_min -= kTileKT;
         held -= kTileKT;
         tmem_wait_st();
         tc_fence_before();
@@ -676,18 +811,15 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         l_sum += ((a0 + a1) + (a2 + a3)) + ((a4 + a5) + (a6 + a7));
       }
       if (!ok) break;
+      more = take(cur);
       if (nt > 0) {
         ok = __all_sync(0xffffffffu, wait(L::kO + x, o_phase));
         if (!ok) break;
         o_phase ^= 1;
         tc_fence_after();
       }
-      const bool whole = sg.k0 == 0 && sg.k1 == sg.x.key_tiles;
       const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;      // no key: zeros
-      const int64_t slot = (int64_t(blockIdx.x) * 2 + (sg.k0 == 0 ? 1 : 0)) * kTileR + x * 128 + r;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t v[32];
+      auto load_o = [&](int c, uint32_t (&v)[32]) {            // 32 channels of this row
         if (nt > 0) {
           tmem_ld32(tO + c * 32, v);
           tmem_wait_ld();
@@ -696,28 +828,52 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0u;
         }
-        if (row.token < 0) continue;
+      };
+      // O by way of the warp's stage, 32 channels of every row at a time: 4 (or,
+      // of an fp32 partial, 8) lanes a row, so that global stores are whole
+      // sectors.  Loops, not unrolled: code that runs once an item costs most
+      // by being fetched.
+      const uint32_t stage = sbase + L::kStage + (warp - 4) * L::kStageBytes;
+      auto stage_at = [&](int w, int c) { return stage + w * 128 + ((c ^ (w & 7)) << 4); };
+      const int lanes_log2 = whole ? 2 : 3;
+      const int w0 = lane >> lanes_log2, wc = lane & ((1 << lanes_log2) - 1);
+      uint64_t to = 0;
+      if (row.token >= 0)
+        to = whole ? reinterpret_cast<uint64_t>(p.out + row.token * p.os[0] + row.head * p.os[1])
+                   : reinterpret_cast<uint64_t>(p.part_o + int64_t(slot) * D);
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t v[32];
+        load_o(c, v);
         if (whole) {
-          uint16_t* o = p.out + row.token * p.os[0] + row.head * p.os[1] + c * 32;
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            uint4 w;
-            w.x = pack2<DT>(__uint_as_float(v[i + 0]) * inv, __uint_as_float(v[i + 1]) * inv);
-            w.y = pack2<DT>(__uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv);
-            w.z = pack2<DT>(__uint_as_float(v[i + 4]) * inv, __uint_as_float(v[i + 5]) * inv);
-            w.w = pack2<DT>(__uint_as_float(v[i + 6]) * inv, __uint_as_float(v[i + 7]) * inv);
-            *reinterpret_cast<uint4*>(o + i) = w;
-          }
-        } else {
-          float* o = p.part_o + slot * D + c * 32;
-#pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<uint4*>(o + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          for (int i = 0; i < 16; ++i)
+            v[i] = pack2<DT>(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < 4 || !whole)
+            st_shared_v4(stage_at(lane, i), make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+        __syncwarp();
+#pragma unroll 1
+        for (int it = 0; it < 1 << lanes_log2; it += 4) {
+          uint4 o[4];
+          uint64_t at[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int w = ((it + q) << (5 - lanes_log2)) + w0;
+            at[q] = __shfl_sync(0xffffffffu, to, w);
+            o[q] = ld_shared_v4(stage_at(w, wc));
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (at[q] != 0) *reinterpret_cast<uint4*>(at[q] + (((c << lanes_log2) + wc) << 4)) = o[q];
+        }
+        __syncwarp();
       }
       if (row.token >= 0) {
         if (!whole)
-          *reinterpret_cast<float2*>(p.part_ml + slot * 2) = make_float2(m_used, l_sum);
+          *reinterpret_cast<float2*>(p.part_ml + int64_t(slot) * 2) = make_float2(m_used, l_sum);
         else if (p.lse != nullptr)
           p.lse[int64_t(row.token) * p.Hq + row.head] =
               l_sum == 0.f ? -INFINITY : (m_used + log2f(l_sum)) * kLn2;
@@ -1063,7 +1219,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       release();
     }
     // the warps' results, each relative to its own maxima, 16 rows at a time
-    const bool whole = cs.k0 == 0 && cs.k1 == cs.x.key_tiles;
+    const bool whole = cs.whole();
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -1142,18 +1298,25 @@ __global__ void __launch_bounds__(2 * JoinShape<R>::kHalf, 4) join_kernel(const 
   auto red_ml = red_ml_all[k];
   const int d0 = (tid % kChunk) * 8, slot = tid / kChunk;
   const Share::Place& at = k ? s.last : s.first;
-  const int units = item_units(p, at.x);
-  const int item = int(((k ? s.u1 - 1 : s.u0) - at.base) / units);
-  const int64_t end = at.base + int64_t(item + 1) * units, begin = end - at.x.key_tiles;   // its key tiles
-  if (begin >= s.u1 || (begin >= s.u0 && end <= s.u1)) return;        // none of them here, or all
-  if (k == 1 && s.u0 >= end - units) return;                           // the first half's item too
-  const int c0 = s.holder(begin), n = s.holder(end - 1) - c0 + 1;                           // its parts' shares
-  if (n == 1) return;
   Segments<R, KT> seg;
   seg.e = at.e;
   seg.x = at.x;
-  seg.h = p.pg.table_heads > 1 ? at.e % p.pg.heads : item / at.x.row_tiles;
-  seg.tile = item % at.x.row_tiles;
+  seg.find(p, at.base, k ? s.u1 - 1 : s.u0);
+  const ItemPlace item = seg.at;
+  if (item.from >= s.u0 && item.to <= s.u1) return;                    // all of it is here
+  if (k == 1 && s.u0 >= item.from) return;                             // the first half's item too
+  const int c0 = s.holder(item.from), n = s.holder(item.to - 1) - c0 + 1;   // the shares that may hold a part
+  // Share c0 + q's key tiles [k0, k1) of the item; none where k0 == k1.
+  auto part = [&](int q, int& k0, int& k1) {
+    k0 = item.tile_at<KT>(p, max(item.from, s.begin(c0 + q)));
+    k1 = item.tile_at<KT>(p, min(item.to, s.begin(c0 + q + 1)));
+  };
+  for (int q = 0; q < n; ++q) {
+    int k0, k1;
+    part(q, k0, k1);
+    if (k0 == 0 && k1 == item.key_tiles) return;                       // one share did it all
+    if (k1 > 0) break;
+  }
   const int rows = min(R, at.x.n * p.G - seg.tile * R);
   const int r_first = c - c0 + int(blockIdx.y) * n, r_step = n * int(gridDim.y);
   const int mine = (rows - r_first + r_step - 1) / r_step;
@@ -1175,8 +1338,10 @@ __global__ void __launch_bounds__(2 * JoinShape<R>::kHalf, 4) join_kernel(const 
           const int q = q0 + b * parts;
           v[b] = make_float2(-INFINITY, 0.f);
           w[b][0] = w[b][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (q < n) {
-            const int64_t from = (int64_t(c0 + q) * 2 + (q == 0 ? 1 : 0)) * R + r;
+          int k0 = 0, k1 = 0;
+          if (q < n) part(q, k0, k1);
+          if (k0 < k1) {
+            const int64_t from = (int64_t(c0 + q) * 2 + (k0 == 0 ? 1 : 0)) * R + r;
             v[b] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + from * 2));
             w[b][0] = __ldcg(reinterpret_cast<const float4*>(p.part_o + from * D + d0));
             w[b][1] = __ldcg(reinterpret_cast<const float4*>(p.part_o + from * D + d0 + 4));
@@ -1236,7 +1401,6 @@ __global__ void __launch_bounds__(2 * JoinShape<R>::kHalf, 4) join_kernel(const 
 // ------------------------------------------------------------------ host side
 constexpr int kPairRows = 12;      // mean rows a (sequence, kv head) above which two row tiles go together
 constexpr int kTileRows = 32;      // mean rows a (sequence, kv head) above which the tiles kernel runs
-constexpr int kWaves = 4;          // items for this many rounds of the device: no split along the keys
 
 static void test_hooks(AttnParams& p) {
   p.wait_limit_ns = kWaitLimitNs;
@@ -1293,13 +1457,12 @@ static int allow_smem(K kern, int smem, std::atomic<uint64_t>* done) {
 }
 
 template <int DT, int D>
-static int launch_tiles(const CUtensorMap& k, const CUtensorMap& v, const AttnParams& p, int64_t grid,
-                        cudaStream_t st) {
+static int launch_tiles(const CUtensorMap& k, const CUtensorMap& v, const AttnParams& p, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   constexpr int smem = TileSmem<D>::kAlloc;
   int rc = allow_smem(tiles_kernel<DT, D>, smem, &done);
-  if (!rc) rc = launch_early(tiles_kernel<DT, D>, dim3(unsigned(grid)), kTileThreads, smem, st, k, v, p);
-  if (rc || !p.split) return rc;
+  if (!rc) rc = launch_early(tiles_kernel<DT, D>, dim3(kCtas), kTileThreads, smem, st, k, v, p);
+  if (rc) return rc;
   using J = JoinShape<kTileR>;
   return launch_early(join_kernel<DT, D, kTileR, kTileKT>, dim3(kCtas, J::kSplit), 2 * J::kHalf, 0, st, p);
 }
@@ -1315,34 +1478,20 @@ static int launch_rows(const CUtensorMap& k, const CUtensorMap& v, const AttnPar
 }
 
 template <int DT>
-static int launch(int D, int rows, const CUtensorMap& k, const CUtensorMap& v, const AttnParams& p, int64_t grid,
-                  cudaStream_t st) {
-  if (rows == kTileR)
-    return D == 128 ? launch_tiles<DT, 128>(k, v, p, grid, st) : launch_tiles<DT, 64>(k, v, p, grid, st);
+static int launch(int D, int rows, const CUtensorMap& k, const CUtensorMap& v, const AttnParams& p, cudaStream_t st) {
+  if (rows == kTileR) return D == 128 ? launch_tiles<DT, 128>(k, v, p, st) : launch_tiles<DT, 64>(k, v, p, st);
   if (rows == 32) return D == 128 ? launch_rows<DT, 128, 2>(k, v, p, st) : launch_rows<DT, 64, 2>(k, v, p, st);
   return D == 128 ? launch_rows<DT, 128, 1>(k, v, p, st) : launch_rows<DT, 64, 1>(k, v, p, st);
 }
 
-// How a call is run, from its shapes alone (the lengths are on the device).
-struct Variant {
-  int rows;                // rows of an item: 256 (tcgen05 tiles), 32 or 16
-  bool split;
-  int64_t items;           // at most this many items
-};
-static Variant choose(int64_t n_tokens, int B, int Hq, int Hkv) {
-  const int64_t G = Hq / Hkv;
-  Variant v;
-  const int64_t rows = n_tokens * G;                  // of a kv head, over all sequences
-  v.rows = rows > int64_t(B) * kTileRows ? kTileR : rows > int64_t(B) * kPairRows ? 32 : 16;
-  v.items = (rows / v.rows + B) * Hkv;
-  v.split = v.rows < kTileR || rows / kTileR * Hkv < int64_t(kWaves) * kCtas;
-  return v;
+// Rows of an item, from the call's shapes alone (the lengths are on the
+// device): 256 (tcgen05 tiles), 32 or 16.
+static int choose_rows(int64_t n_tokens, int B, int Hq, int Hkv) {
+  const int64_t rows = n_tokens * (Hq / Hkv);         // of a kv head, over all sequences
+  return rows > int64_t(B) * kTileRows ? kTileR : rows > int64_t(B) * kPairRows ? 32 : 16;
 }
 
-static int64_t workspace_bytes_for(const Variant& v, int D) {
-  if (!v.split) return 16;
-  return int64_t(kCtas) * 2 * v.rows * (D + 2) * 4;
-}
+static int64_t workspace_bytes_for(int rows, int D) { return int64_t(kCtas) * 2 * rows * (D + 2) * 4; }
 
 }  // namespace paged
 }  // namespace vark
@@ -1355,7 +1504,7 @@ extern "C" int64_t vark_paged_attention_workspace(int64_t n_tokens, int B, int H
   if (D != 64 && D != 128) return VARK_E_SHAPE;
   if (n_tokens < 0 || B < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || page_size < 1 || max_pages < 1)
     return VARK_E_SHAPE;
-  return workspace_bytes_for(choose(n_tokens, B, Hq, Hkv), D);
+  return workspace_bytes_for(choose_rows(n_tokens, B, Hq, Hkv), D);
 }
 
 extern "C" int vark_paged_attention(int dtype, const uint16_t* q, const int64_t* q_strides, int64_t n_tokens, int B,
@@ -1389,12 +1538,10 @@ extern "C" int vark_paged_attention(int dtype, const uint16_t* q, const int64_t*
   p.N = n_tokens;
   p.B = B; p.G = Hq / Hkv; p.Hq = Hq; p.causal = causal != 0;
   p.scale_log2 = kLog2e / sqrtf(float(D));
-  const Variant var = choose(n_tokens, B, Hq, Hkv);
-  if (var.items > INT32_MAX) return VARK_E_SHAPE;
-  p.split = var.split;
-  p.item_cost = var.rows < kTileR && D == 64 ? 3 : 1;    // 2300-4000 cycles; a tile takes 2400 (D = 64: 1400)
+  const int rows = choose_rows(n_tokens, B, Hq, Hkv);
+  p.item_cost = rows == kTileR || D == 64 ? 3 : 1;   // measured best of 0 (1) to 4
   p.part_ml = static_cast<float*>(workspace);
-  p.part_o = p.part_ml + int64_t(kCtas) * 2 * var.rows * 2;
+  p.part_o = p.part_ml + int64_t(kCtas) * 2 * rows * 2;
   p.status = dev_status;
   test_hooks(p);
   const int box = page_size < kTileKT ? page_size : kTileKT;
@@ -1402,7 +1549,5 @@ extern "C" int vark_paged_attention(int dtype, const uint16_t* q, const int64_t*
   if ((rc = encode_pages(&tk, k_pages, p.pg, D, box))) return rc;
   if ((rc = encode_pages(&tv, v_pages, p.pg, D, box))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int64_t grid = var.split ? kCtas : var.items;
-  return dtype == VARK_BF16 ? launch<VARK_BF16>(D, var.rows, tk, tv, p, grid, st)
-                            : launch<VARK_FP16>(D, var.rows, tk, tv, p, grid, st);
+  return dtype == VARK_BF16 ? launch<VARK_BF16>(D, rows, tk, tv, p, st) : launch<VARK_FP16>(D, rows, tk, tv, p, st);
 }

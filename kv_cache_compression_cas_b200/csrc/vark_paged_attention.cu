@@ -1270,66 +1270,77 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
 }
 
 // Joins partial results.  The CTAs whose shares hold a part of an item share its
-// rows: share c takes every n-th of them, n the number of parts (dealt on to the
-// gridDim.y CTAs of the share), and finds at most two such items, at its two
-// ends: one for each half of its threads.  Threads that a few rows would leave
-// idle share the parts of a row.  (The CTA waits beside a running rows kernel,
-// in the registers that leaves.  One CTA per item took 5 us for 19 parts.)
+// rows, 32 channels at a time: share c takes every n-th of these pieces, n the
+// number of parts (dealt on to the gridDim.y CTAs of the share), and finds at
+// most two such items, at its two ends: one for each half of its threads.
+// Threads that a few pieces would leave idle share the parts of one.  All that
+// does not need the partials is done before the attention ends; the CTA waits
+// beside a running rows kernel, in the registers that leaves.  (One CTA per
+// item took 5 us for 19 parts, a row a CTA 4.)
 template <int R>
 struct JoinShape { static constexpr int kHalf = 128, kSplit = R == kTileR ? 4 : 1; };
 
 template <int DT, int D, int R, int KT>
 __global__ void __launch_bounds__(2 * JoinShape<R>::kHalf, 4) join_kernel(const __grid_constant__ AttnParams p) {
   constexpr int kHalf = JoinShape<R>::kHalf;
-  constexpr int kChunk = D / 8;                     // threads of a row, 8 channels each
-  constexpr int kRowSlots = kHalf / kChunk;     // (row, part) slots
-  __shared__ __align__(16) float red_all[2][kRowSlots][D + 4];
-  __shared__ float red_ml_all[2][kRowSlots][2];
+  constexpr int kPieces = D / 32;               // of a row
+  constexpr int kSlots = kHalf / 4;             // (piece, part) slots of 4 threads, 8 channels each
+  __shared__ __align__(16) float red_all[2][kSlots][32 + 4];
+  __shared__ float red_ml_all[2][kSlots][2];
   const int c = blockIdx.x;
   grid_release();
   const Share s = find_share<R, KT, 2 * kHalf, true>(p, c);
-  // Every CTA waits, also those without an item: the launch after this one
-  // may count on the attention kernel's end.
-  grid_wait();
-  if (s.u0 == s.u1) return;
-  const int32_t status = *reinterpret_cast<volatile int32_t*>(p.status);
   const int k = threadIdx.x / kHalf, tid = threadIdx.x % kHalf;
   auto red = red_all[k];
   auto red_ml = red_ml_all[k];
-  const int d0 = (tid % kChunk) * 8, slot = tid / kChunk;
-  const Share::Place& at = k ? s.last : s.first;
+  const int d1 = (tid & 3) * 8, slot = tid >> 2;
   Segments<R, KT> seg;
-  seg.e = at.e;
-  seg.x = at.x;
-  seg.find(p, at.base, k ? s.u1 - 1 : s.u0);
-  const ItemPlace item = seg.at;
-  if (item.from >= s.u0 && item.to <= s.u1) return;                    // all of it is here
-  if (k == 1 && s.u0 >= item.from) return;                             // the first half's item too
-  const int c0 = s.holder(item.from), n = s.holder(item.to - 1) - c0 + 1;   // the shares that may hold a part
+  ItemPlace item = {0, 0, 0};
+  int c0 = 0, n = 0;                            // the shares that may hold a part
   // Share c0 + q's key tiles [k0, k1) of the item; none where k0 == k1.
   auto part = [&](int q, int& k0, int& k1) {
     k0 = item.tile_at<KT>(p, max(item.from, s.begin(c0 + q)));
     k1 = item.tile_at<KT>(p, min(item.to, s.begin(c0 + q + 1)));
   };
-  for (int q = 0; q < n; ++q) {
-    int k0, k1;
-    part(q, k0, k1);
-    if (k0 == 0 && k1 == item.key_tiles) return;                       // one share did it all
-    if (k1 > 0) break;
+  bool work = s.u0 != s.u1;
+  if (work) {
+    const Share::Place& at = k ? s.last : s.first;
+    seg.e = at.e;
+    seg.x = at.x;
+    seg.find(p, at.base, k ? s.u1 - 1 : s.u0);
+    item = seg.at;
+    if (item.from >= s.u0 && item.to <= s.u1) work = false;             // all of it is here
+    if (k == 1 && s.u0 >= item.from) work = false;                       // the first half's item too
   }
-  const int rows = min(R, at.x.n * p.G - seg.tile * R);
-  const int r_first = c - c0 + int(blockIdx.y) * n, r_step = n * int(gridDim.y);
-  const int mine = (rows - r_first + r_step - 1) / r_step;
-  for (int r0 = 0; r0 < mine; r0 += kRowSlots) {
-    int width = 1;                                 // row slots of a part
-    while (width < min(kRowSlots, mine - r0)) width *= 2;
-    const int parts = kRowSlots / width;
-    const int i0 = r0 + slot % width, r = r_first + i0 * r_step;
+  if (work) {
+    c0 = s.holder(item.from);
+    n = s.holder(item.to - 1) - c0 + 1;
+    for (int q = 0; q < n; ++q) {
+      int k0, k1;
+      part(q, k0, k1);
+      if (k0 == 0 && k1 == item.key_tiles) work = false;                 // one share did it all
+      if (k1 > 0) break;
+    }
+  }
+  const int pieces = work ? min(R, seg.x.n * p.G - seg.tile * R) * kPieces : 0;
+  const int first = c - c0 + int(blockIdx.y) * n, step = n * int(gridDim.y);
+  const int mine = work ? (pieces - first + step - 1) / step : 0;
+  // Every CTA waits, also those without an item: the launch after this one
+  // may count on the attention kernel's end.
+  grid_wait();
+  if (mine <= 0) return;
+  const int32_t status = *reinterpret_cast<volatile int32_t*>(p.status);
+  for (int r0 = 0; r0 < mine; r0 += kSlots) {
+    int width = 1;                              // slots of a part
+    while (width < min(kSlots, mine - r0)) width *= 2;
+    const int parts = kSlots / width;
+    const int i0 = r0 + slot % width, piece = first + i0 * step;
+    const int r = piece / kPieces, d0 = piece % kPieces * 32 + d1;
     float top = -INFINITY, sum = 0.f, acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
     if (i0 < mine) {
-      constexpr int kBatch = 2;                    // partials in flight a thread
+      constexpr int kBatch = 2;                 // partials in flight a thread
       for (int q0 = slot / width; q0 < n; q0 += kBatch * parts) {
         float2 v[kBatch];
         float4 w[kBatch][2];
@@ -1371,8 +1382,8 @@ __global__ void __launch_bounds__(2 * JoinShape<R>::kHalf, 4) join_kernel(const 
       named_bar_sync(1 + k, kHalf);
 #pragma unroll
       for (int e = 0; e < 8; e += 4)
-        *reinterpret_cast<float4*>(&red[slot][d0 + e]) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
-      if (d0 == 0) {
+        *reinterpret_cast<float4*>(&red[slot][d1 + e]) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+      if (d1 == 0) {
         red_ml[slot][0] = top;
         red_ml[slot][1] = sum;
       }
@@ -1386,11 +1397,12 @@ __global__ void __launch_bounds__(2 * JoinShape<R>::kHalf, 4) join_kernel(const 
         sum *= own;
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] *= own;
+#pragma unroll 4
         for (int q = 1; q < parts; ++q) {
           const float wgt = ex2_approx(red_ml[slot + q * width][0] - ref);
           sum = fmaf(red_ml[slot + q * width][1], wgt, sum);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc[e] = fmaf(red[slot + q * width][d0 + e], wgt, acc[e]);
+          for (int e = 0; e < 8; ++e) acc[e] = fmaf(red[slot + q * width][d1 + e], wgt, acc[e]);
         }
       }
     }

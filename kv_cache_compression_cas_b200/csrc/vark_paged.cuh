@@ -70,8 +70,8 @@ inline int make_pages(Pages* p, const int32_t* table, const int32_t* len, int64_
                       int max_pages, int H, int head_pages) {
   if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128 && page_size != 256)
     return VARK_E_SHAPE;
-  if (n_pages < 1 || n_pages > INT32_MAX || max_pages < 1 || int64_t(max_pages) * page_size > INT32_MAX)
-    return VARK_E_SHAPE;
+  if (n_pages < 1 || n_pages > INT32_MAX || max_pages < 1) return VARK_E_SHAPE;
+  if (int64_t(max_pages) * page_size > INT32_MAX - 1024) return VARK_E_SHAPE;   // key indices, and a tile past them
   p->table = table;
   p->len = len;
   p->n_pages = n_pages;

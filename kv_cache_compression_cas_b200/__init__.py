@@ -5,6 +5,9 @@ Argument marshalling only -- every step of the path runs in the CUDA library
 `libvark.so` built in-tree from `csrc/` (see `build.py`).  Functions carry the
 C names; torch tensors supply device memory, `torch.cuda.current_stream()`
 the stream.  A missing library raises at first use; there is no fallback.
+The serving calls, whose smallest take less time on the device than a careful
+call takes in Python, go through the module `_paged_call` where it is built;
+it hands every call that is not plainly right back to the functions here.
 """
 from __future__ import annotations
 
@@ -679,6 +682,31 @@ def _call_on(dev, stream, fn, *args):
         return fn(*args, _stream(stream))
 
 
+def _quick():
+    """The marshalling module, bound to the library; False where it is not
+    built (the calls then go through the functions below)."""
+    global _quick_module
+    if _quick_module is None:
+        _torch()
+        lib = _load()
+        try:
+            from . import _paged_call as module
+        except ImportError:
+            module = False
+        else:
+            module.bind(*(ctypes.cast(f, _P).value
+                          for f in (lib.vark_qk_norm_rope, lib.vark_paged_append, lib.vark_paged_attention)))
+        _quick_module = module
+    return _quick_module
+
+
+_quick_module = None
+
+
+def _handle(stream):
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+
+
 def _torch():
     global _torch_module
     if _torch_module is None:
@@ -722,6 +750,12 @@ def vark_qk_norm_rope(q, k, q_out, k_out, norm: int, q_weight, k_weight, eps: fl
     any strides but the channels', outputs alike; either may be None (its
     output and weight then too); weights fp32 [D] or None; rope fp32
     [positions][2][rope_dim / 2] and positions int32 [B][T], or both None."""
+    quick = _quick_module or _quick()
+    if quick:
+        rc = quick.norm_rope(q, k, q_out, k_out, norm, q_weight, k_weight, eps, rope, positions, dev_status, pairs,
+                             None if stream is None else _handle(stream))
+        if rc is not None:
+            return _check(rc, "vark_qk_norm_rope")
     torch = _torch()
     f32, i32 = torch.float32, torch.int32
     x = q if q is not None else k
@@ -785,6 +819,12 @@ def vark_paged_append(k, v, cu_tokens, k_pages, v_pages, page_table, cache_len, 
     [B][max_pages] and cache_len [B], or head-specific pools
     [pages][page_size][D] with [B][H][max_pages] and [B][H]; cu_tokens int32
     [B + 1]; rope and positions (int32 [tokens]) as vark_qk_norm_rope."""
+    quick = _quick_module or _quick()
+    if quick:
+        rc = quick.append(k, v, cu_tokens, k_pages, v_pages, page_table, cache_len, norm, k_weight, eps, rope,
+                          positions, dev_status, pairs, None if stream is None else _handle(stream))
+        if rc is not None:
+            return _check(rc, "vark_paged_append")
     torch = _torch()
     shape = n, H, D = _rank(k, 3, "k")
     dt = _paged_dtype(k, "k")
@@ -817,6 +857,12 @@ def vark_paged_attention(q, cu_tokens, k_pages, v_pages, page_table, cache_len, 
     q, out [tokens][Hq][D] with any strides but the channels'; pools, tables and
     lengths as vark_paged_append; tau fp32 [Hq] or None; lse fp32 [tokens][Hq]
     or None; workspace uint8 of vark_paged_attention_workspace bytes."""
+    quick = _quick_module or _quick()
+    if quick:
+        rc = quick.attention(q, cu_tokens, k_pages, v_pages, page_table, cache_len, tau, causal, out, lse, workspace,
+                             dev_status, None if stream is None else _handle(stream))
+        if rc is not None:
+            return _check(rc, "vark_paged_attention")
     torch = _torch()
     shape = n, Hq, D = _rank(q, 3, "q")
     dt = _paged_dtype(q, "q")

@@ -1,15 +1,19 @@
 """Builds the in-tree shared library `libvark.so` from `csrc/` with nvcc for
-sm_100a only.  Objects go to `_build/` at the repository root; a source is
-recompiled when it or any header is newer than its object.
+sm_100a only, and the Python module `_paged_call.so` (argument marshalling of
+the serving calls, against torch's headers) from `binding/`.  Objects go to
+`_build/` at the repository root; a source is recompiled when it or any header
+is newer than its object.
 
     python -m kv_cache_compression_cas_b200.build [--force] [--verbose]
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libvark.so")
+CALL_SRC = os.path.join(PKG, "binding", "paged_call.cpp")
+CALL = os.path.join(PKG, "_paged_call.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -63,6 +69,29 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def build_call(force: bool = False, verbose: bool = False) -> str:
+    newest = max(os.path.getmtime(f) for f in (CALL_SRC, os.path.join(INCLUDE, "vark.h")))
+    if not force and os.path.exists(CALL) and os.path.getmtime(CALL) >= newest:
+        return CALL
+    spec = importlib.util.find_spec("torch")       # located, not imported
+    torch_dir = os.path.dirname(spec.origin)
+    inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-DNDEBUG", f"-I{sysconfig.get_paths()['include']}",
+           f"-I{inc}", f"-I{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}",
+           f"-I{os.path.join(cuda, 'include')}", f"-I{INCLUDE}", CALL_SRC, "-o", CALL, f"-L{lib}", "-ltorch_python",
+           "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose or r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed on paged_call.cpp")
+    return CALL
+
+
 if __name__ == "__main__":
     build(force="--force" in sys.argv, verbose="--verbose" in sys.argv)
     print(LIB)
+    print(build_call(force="--force" in sys.argv, verbose="--verbose" in sys.argv))

@@ -162,6 +162,8 @@ __global__ void __launch_bounds__(kRowThreads) norm_rope_kernel(const __grid_con
   constexpr int kLanes = D / 16, kRows = 32 / kLanes, kIters = kQkHeads / kRows;
   const int lane = threadIdx.x & 31, li = lane % kLanes;
   const int token = int(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
+  grid_release();
+  grid_wait();
   if (token >= p.tokens) return;
   const bool keys = int(blockIdx.y) >= p.q_blocks;
   const RowTensor& t = p.t[keys];
@@ -241,6 +243,8 @@ __global__ void __launch_bounds__(kRowThreads, 12) append_kernel(const __grid_co
   constexpr int kLanes = D / 16, kRows = 32 / kLanes, kIters = (kKvHeads + kRows - 1) / kRows;
   const int lane = threadIdx.x & 31, li = lane % kLanes;
   const int token = int(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
+  grid_release();
+  grid_wait();
   if (token >= p.tokens) return;
   const int h0 = int(blockIdx.y) * kKvHeads + lane / kLanes;
   Lane<D> ln;
@@ -373,14 +377,11 @@ extern "C" int vark_qk_norm_rope(int dtype, const uint16_t* q, const int64_t* q_
   p.q_blocks = blocks_of(p.t[0].heads, kQkHeads);
   const dim3 grid = token_grid(p.tokens, p.q_blocks + blocks_of(p.t[1].heads, kQkHeads));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dtype == VARK_BF16) {
-    if (D == 128) norm_rope_kernel<VARK_BF16, 128><<<grid, kRowThreads, 0, st>>>(p);
-    else norm_rope_kernel<VARK_BF16, 64><<<grid, kRowThreads, 0, st>>>(p);
-  } else {
-    if (D == 128) norm_rope_kernel<VARK_FP16, 128><<<grid, kRowThreads, 0, st>>>(p);
-    else norm_rope_kernel<VARK_FP16, 64><<<grid, kRowThreads, 0, st>>>(p);
-  }
-  return cudaGetLastError() == cudaSuccess ? VARK_OK : VARK_E_CUDA;
+  if (dtype == VARK_BF16)
+    return D == 128 ? launch_early(norm_rope_kernel<VARK_BF16, 128>, grid, kRowThreads, 0, st, p)
+                    : launch_early(norm_rope_kernel<VARK_BF16, 64>, grid, kRowThreads, 0, st, p);
+  return D == 128 ? launch_early(norm_rope_kernel<VARK_FP16, 128>, grid, kRowThreads, 0, st, p)
+                  : launch_early(norm_rope_kernel<VARK_FP16, 64>, grid, kRowThreads, 0, st, p);
 }
 
 extern "C" int vark_paged_append(int dtype, const uint16_t* k, const int64_t* k_strides, const uint16_t* v,
@@ -416,12 +417,9 @@ extern "C" int vark_paged_append(int dtype, const uint16_t* k, const int64_t* k_
   p.status = dev_status;
   const dim3 grid = token_grid(n_tokens, blocks_of(H, kKvHeads));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dtype == VARK_BF16) {
-    if (D == 128) append_kernel<VARK_BF16, 128><<<grid, kRowThreads, 0, st>>>(p);
-    else append_kernel<VARK_BF16, 64><<<grid, kRowThreads, 0, st>>>(p);
-  } else {
-    if (D == 128) append_kernel<VARK_FP16, 128><<<grid, kRowThreads, 0, st>>>(p);
-    else append_kernel<VARK_FP16, 64><<<grid, kRowThreads, 0, st>>>(p);
-  }
-  return cudaGetLastError() == cudaSuccess ? VARK_OK : VARK_E_CUDA;
+  if (dtype == VARK_BF16)
+    return D == 128 ? launch_early(append_kernel<VARK_BF16, 128>, grid, kRowThreads, 0, st, p)
+                    : launch_early(append_kernel<VARK_BF16, 64>, grid, kRowThreads, 0, st, p);
+  return D == 128 ? launch_early(append_kernel<VARK_FP16, 128>, grid, kRowThreads, 0, st, p)
+                  : launch_early(append_kernel<VARK_FP16, 64>, grid, kRowThreads, 0, st, p);
 }

@@ -10,6 +10,32 @@ namespace paged {
 // Records the first error of a call in the caller's status word.
 VARK_DEV void record(int32_t* status, int32_t code) { atomicCAS(status, 0, code); }
 
+// Dependent launches.  A call's kernels, and calls that follow one another,
+// overlap at their ends: a kernel lets the next one start early, and the next
+// one waits for it (and all before it) before it touches what it may have
+// written.
+VARK_DEV void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+VARK_DEV void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launch that may start before the kernels ahead of it have ended (see
+// grid_wait).
+template <typename K, typename... A>
+inline int launch_early(K kern, dim3 grid, int threads, int smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess) return VARK_OK;
+  cudaGetLastError();
+  return VARK_E_CUDA;
+}
+
 // Two 16-bit values of element type DT (VARK_BF16, VARK_FP16) to and from fp32.
 template <int DT>
 VARK_DEV void unpack2(uint32_t w, float& lo, float& hi) {

@@ -45,13 +45,6 @@ struct AttnParams {
   int withhold;            // test hook: slices a warp loads before it stops (-1: all)
 };
 
-// Dependent launches.  A call's two kernels, and calls that follow one another,
-// overlap at their ends: a kernel lets the next one start early, and the next
-// one waits for it (and all before it) before it touches what it may have
-// written.
-VARK_DEV void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-VARK_DEV void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // ------------------------------------------------------------------ the plan
 // An entry is one row of the length table: a sequence (shared pages, all kv
 // heads) or a (sequence, head).  Its items, head after head and row tile after
@@ -1432,25 +1425,6 @@ static int encode_pages(CUtensorMap* m, const uint16_t* base, const Pages& pg, i
   const uint64_t dims[3] = {uint64_t(D), rows, uint64_t(pg.n_pages)};
   const uint64_t strides[2] = {uint64_t(D) * 2, rows * D * 2};
   return encode_bf16_map(m, base, 3, dims, strides, uint32_t(box_rows));   // 16-bit elements, copied as they are
-}
-
-// Launch that may start before the kernels ahead of it have ended (see
-// grid_wait).
-template <typename K, typename... A>
-static int launch_early(K kern, dim3 grid, int threads, int smem, cudaStream_t st, const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(unsigned(threads));
-  cfg.dynamicSmemBytes = size_t(smem);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess) return VARK_OK;
-  cudaGetLastError();
-  return VARK_E_CUDA;
 }
 
 // Lets a kernel use more than 48 KB of shared memory; asked for once a device.

@@ -1404,8 +1404,16 @@ __global__ void __launch_bounds__(2 * JoinShape<R>::kHalf, 4) join_kernel(const 
 }
 
 // ------------------------------------------------------------------ host side
-constexpr int kPairRows = 12;      // mean rows a (sequence, kv head) above which two row tiles go together
-constexpr int kTileRows = 32;      // mean rows a (sequence, kv head) above which the tiles kernel runs
+// Rows of an item, from the call's shapes alone (the lengths are on the
+// device): the mean rows a (sequence, kv head) decide.  Up to 16 one row tile
+// (16 rows over 2 x 20000 keys, D = 128: 27 us against 30 as two tiles and 43
+// on tcgen05); up to 32 two (20 rows: 31, 33 as one at a time, 42); D = 64 two
+// at a time up to 64 (64 rows: 32 against 35 on tcgen05, 96: 41 against 34);
+// beyond that 256 on tcgen05 (D = 128, 48 rows: 43 against 45; 96: 44 against 59).
+static int choose_rows(int64_t n_tokens, int B, int Hq, int Hkv, int D) {
+  const int64_t rows = n_tokens * (Hq / Hkv);         // of a kv head, over all sequences
+  return rows <= int64_t(B) * 16 ? 16 : rows <= int64_t(B) * (D == 64 ? 64 : 32) ? 32 : kTileR;
+}
 
 static void test_hooks(AttnParams& p) {
   p.wait_limit_ns = kWaitLimitNs;
@@ -1470,13 +1478,6 @@ static int launch(int D, int rows, const CUtensorMap& k, const CUtensorMap& v, c
   return D == 128 ? launch_rows<DT, 128, 1>(k, v, p, st) : launch_rows<DT, 64, 1>(k, v, p, st);
 }
 
-// Rows of an item, from the call's shapes alone (the lengths are on the
-// device): 256 (tcgen05 tiles), 32 or 16.
-static int choose_rows(int64_t n_tokens, int B, int Hq, int Hkv) {
-  const int64_t rows = n_tokens * (Hq / Hkv);         // of a kv head, over all sequences
-  return rows > int64_t(B) * kTileRows ? kTileR : rows > int64_t(B) * kPairRows ? 32 : 16;
-}
-
 static int64_t workspace_bytes_for(int rows, int D) { return int64_t(kCtas) * 2 * rows * (D + 2) * 4; }
 
 }  // namespace paged
@@ -1490,7 +1491,7 @@ extern "C" int64_t vark_paged_attention_workspace(int64_t n_tokens, int B, int H
   if (D != 64 && D != 128) return VARK_E_SHAPE;
   if (n_tokens < 0 || B < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || page_size < 1 || max_pages < 1)
     return VARK_E_SHAPE;
-  return workspace_bytes_for(choose_rows(n_tokens, B, Hq, Hkv), D);
+  return workspace_bytes_for(choose_rows(n_tokens, B, Hq, Hkv, D), D);
 }
 
 extern "C" int vark_paged_attention(int dtype, const uint16_t* q, const int64_t* q_strides, int64_t n_tokens, int B,
@@ -1524,7 +1525,7 @@ extern "C" int vark_paged_attention(int dtype, const uint16_t* q, const int64_t*
   p.N = n_tokens;
   p.B = B; p.G = Hq / Hkv; p.Hq = Hq; p.causal = causal != 0;
   p.scale_log2 = kLog2e / sqrtf(float(D));
-  const int rows = choose_rows(n_tokens, B, Hq, Hkv);
+  const int rows = choose_rows(n_tokens, B, Hq, Hkv, D);
   p.item_cost = rows == kTileR || D == 64 ? 3 : 1;   // measured best of 0 (1) to 4
   p.part_ml = static_cast<float*>(workspace);
   p.part_o = p.part_ml + int64_t(kCtas) * 2 * rows * 2;

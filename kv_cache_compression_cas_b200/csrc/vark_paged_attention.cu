@@ -26,6 +26,22 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;       // log2: a running maximum may lag by this much
 
+// Division by a number the host knows, by a product (a division costs 130
+// cycles of latency, and several lie on the way to a CTA's first load).  Of
+// the divisor d, with s = ceil(log2 d): mul = floor(2^32 (2^s - d) / d) + 1;
+// x / d = (hi32(x mul) + x) >> s for 0 <= x < 2^31.
+struct FastDiv {
+  uint32_t mul, shift;
+  static FastDiv of(int d) {
+    FastDiv f;
+    f.shift = 0;
+    while ((uint32_t(1) << f.shift) < uint32_t(d)) ++f.shift;
+    f.mul = uint32_t(((uint64_t(1) << 32) * ((uint64_t(1) << f.shift) - uint32_t(d))) / uint32_t(d) + 1);
+    return f;
+  }
+  VARK_DEV int operator()(int x) const { return int((__umulhi(uint32_t(x), mul) + uint32_t(x)) >> shift); }
+};
+
 struct AttnParams {
   const uint16_t* q;
   uint16_t* out;
@@ -36,6 +52,9 @@ struct AttnParams {
   const float* tau;        // [Hq] or null
   int64_t N;
   int B, G, Hq, causal;
+  FastDiv by_group, by_heads;   // / G, / kv heads
+  int tokens_per_tile;     // R / G
+  int tile_step;           // kUnit R / G: weight from a row tile to the next under a causal mask
   int item_cost;           // key tiles that an item counts for besides its own
   float scale_log2;        // log2(e) / sqrt(D)
   float* part_o;           // [kCtas][2][R][D]
@@ -91,7 +110,7 @@ struct Entry {
 template <int R, int KT>
 VARK_DEV Entry load_entry(const AttnParams& p, int e) {
   Entry x;
-  const int b = e / p.pg.table_heads;
+  const int b = p.pg.table_heads > 1 ? p.by_heads(e) : e;
   x.first = p.cu[b];
   const int end = p.cu[b + 1];
   x.len = p.pg.len[e];
@@ -103,8 +122,8 @@ VARK_DEV Entry load_entry(const AttnParams& p, int e) {
   }
   x.row_tiles = (x.n * p.G + R - 1) / R;
   x.heads = p.pg.table_heads > 1 ? 1 : p.pg.heads;
-  x.slope = p.causal && x.row_tiles > 1 ? R * kUnit / p.G : 0;
-  const int seen0 = x.slope ? min(x.len, max(0, x.len - x.n) + R / p.G) : x.len;     // by the first row tile
+  x.slope = p.causal && x.row_tiles > 1 ? p.tile_step : 0;
+  const int seen0 = x.slope ? min(x.len, max(0, x.len - x.n) + p.tokens_per_tile) : x.len;     // by the first row tile
   x.weight0 = int64_t(kUnit) * (int64_t(p.item_cost) * KT + seen0);
   return x;
 }
@@ -255,14 +274,14 @@ struct Segments {
     place(p);
   }
   VARK_DEV void place(const AttnParams& p) {
-    h = p.pg.table_heads > 1 ? e % p.pg.heads : i;
+    h = p.pg.table_heads > 1 ? e - p.by_heads(e) * p.pg.heads : i;
     at.to = at.from + x.weight0 + int64_t(tile) * x.slope;
     at.key_tiles = max(1, (limit(p) + KT - 1) / KT);
   }
   // Keys that some row of the tile sees.
   VARK_DEV int limit(const AttnParams& p) const {
     if (!p.causal) return x.len;
-    const int last = min(x.n - 1, (tile * R + R - 1) / p.G);
+    const int last = min(x.n - 1, p.by_group(tile * R + R - 1));
     return max(0, x.len - x.n + last + 1);
   }
 };
@@ -275,7 +294,7 @@ template <int R, int KT>
 VARK_DEV RowAt row_at(const AttnParams& p, const Segments<R, KT>& s, int r) {
   RowAt a;
   const int row = s.tile * R + r;
-  const int t = row / p.G;
+  const int t = p.by_group(row);
   a.head = s.h * p.G + (row - t * p.G);
   a.token = t < s.x.n ? s.x.first + t : -1;
   a.limit = t >= s.x.n ? 0 : p.causal ? s.x.len - s.x.n + t + 1 : s.x.len;
@@ -1524,9 +1543,13 @@ extern "C" int vark_paged_attention(int dtype, const uint16_t* q, const int64_t*
   p.tau = tau;
   p.N = n_tokens;
   p.B = B; p.G = Hq / Hkv; p.Hq = Hq; p.causal = causal != 0;
+  p.by_group = FastDiv::of(p.G);
+  p.by_heads = FastDiv::of(Hkv);
   p.scale_log2 = kLog2e / sqrtf(float(D));
   const int rows = choose_rows(n_tokens, B, Hq, Hkv, D);
   p.item_cost = rows == kTileR || D == 64 ? 3 : 1;   // measured best of 0 (1) to 4
+  p.tokens_per_tile = rows / p.G;
+  p.tile_step = rows * kUnit / p.G;
   p.part_ml = static_cast<float*>(workspace);
   p.part_o = p.part_ml + int64_t(kCtas) * 2 * rows * 2;
   p.status = dev_status;

@@ -548,8 +548,10 @@ int vark_pruned_attention_int3(const uint16_t* q, const uint8_t* kq, const uint8
  *   dtype as well, as the calls above do).
  * Chunk: the new tokens of all sequences one behind another; cu_tokens (dev
  *   int32 [B + 1], ascending from 0) gives their bounds, sequence b holding
- *   tokens cu_tokens[b] .. cu_tokens[b + 1] - 1, possibly none.  Tokens from
- *   cu_tokens[B] on are padding: their outputs are not written.
+ *   tokens cu_tokens[b] .. cu_tokens[b + 1] - 1, possibly none.  Tokens of no
+ *   sequence (from cu_tokens[B] on) are padding: their outputs are not written.
+ *   A call without tokens or without sequences does nothing; its tensors may
+ *   be NULL.
  * Pool: k_pages, v_pages dev [n_pages][H][page_size][D], page_size 16, 32, 64,
  *   128 or 256.  With head_pages = 1 a page holds rows of a single head,
  *   [n_pages][page_size][D], and every (sequence, head) has its own list and
@@ -564,8 +566,9 @@ int vark_pruned_attention_int3(const uint16_t* q, const uint8_t* kq, const uint8
  *   last cache_len tokens of the chunk.
  * Sequences may share pages that are only read; the rows of one append must be
  * distinct.  Tables that leave the arguments' ranges (offsets outside
- * [0, n_tokens] or descending, cache_len outside [0, max_pages * page_size], a
- * page in use outside [0, n_pages), a position behind the rotation table) set
+ * [0, n_tokens] or descending; cache_len outside [0, max_pages * page_size], in
+ * an append that of a sequence with tokens; a page that is read or written
+ * outside [0, n_pages); a position behind the rotation table) set
  * *dev_status to VARK_E_SHAPE; nothing outside the arguments is touched, the
  * rows concerned are not stored (norm, append), the attention's outputs are
  * unspecified.
@@ -590,10 +593,12 @@ enum vark_norm {
  *                read, and the [B][H][T][D] of the dense attention calls
  *                written, in place.  Either may be NULL (with its strides,
  *                output and weight).
- *   q_out, k_out dev, by their own strides; may be q, k themselves (same
- *                strides), else they must not overlap the inputs.
+ *   q_out, k_out dev, by their own strides (at least D: no two rows at one
+ *                place); may be q, k themselves (same strides), else they must
+ *                not overlap the inputs.
  *   B, T         >= 0, B * T < 2^31 - 128;  Hq, Hk >= 1, <= 65536;  D 64 or 128.
- *   norm         vark_norm;  eps >= 0.
+ *   norm         vark_norm;  eps >= 0 (L2: 0 or a normal number).  A row of
+ *                zeros with eps = 0 has no norm and gives NaN.
  *   q_weight, k_weight  dev fp32 [D], or NULL for ones.
  *   rope         dev fp32 [rope_len][2][rope_dim / 2]: a position's cosines,
  *                then its sines (any angles: one axis, or the 2-D angles of a
@@ -604,7 +609,7 @@ enum vark_norm {
  *   positions    dev int32 [B][T], given exactly when rope is; a token whose
  *                position is negative is padding: its outputs are not written.
  * The squares of a row are summed in fp32: rows whose norm passes 1.8e19
- *   (bf16 only) overflow.
+ *   (bf16 only) overflow, channels below 1e-19 count for less or nothing.
  * Errors: VARK_E_ARG, VARK_E_SHAPE, VARK_E_ALIGN, VARK_E_CUDA, VARK_E_DEVICE.
  */
 int vark_qk_norm_rope(int dtype, const uint16_t* q, const int64_t* q_strides, uint16_t* q_out,
@@ -650,7 +655,8 @@ int64_t vark_paged_attention_workspace(int64_t n_tokens, int B, int Hq, int Hkv,
  * Logit tau[h] * (q . k) / sqrt(D); softmax over the rows seen.  A query that
  * sees no row gets a zero output and -inf in lse.
  *   q, out       dev 16-bit; the row of (token, head) starts at token *
- *                strides[0] + head * strides[1] (as vark_paged_append).
+ *                strides[0] + head * strides[1] (as vark_paged_append; those of
+ *                out at least D); out must not overlap q.
  *   tau          dev fp32 [Hq] or NULL (ones).
  *   lse          dev fp32 [n_tokens][Hq] out, or NULL: log of the sum of exp of
  *                the logits, with which outputs over disjoint caches combine.

@@ -648,8 +648,16 @@ def _strides_fit(t, rows):
     st, shape = t.stride(), t.shape
     if st[-1] != 1:
         return False
-    # an output's rows must not overlap (an axis of one entry has no step)
-    return rows == 1 or all(n <= 1 or s >= shape[-1] for n, s in zip(shape[:-1], st[:-1]))
+    if rows == 1:
+        return True
+    # an output's rows must not overlap: from the smallest stride on, every
+    # axis steps over all that the ones before it span
+    span = shape[-1]
+    for step, n in sorted((s, n) for s, n in zip(st[:-1], shape[:-1]) if n > 1):
+        if step < span:
+            return False
+        span += step * (n - 1)
+    return True
 
 
 def _refuse(dev, specs):
@@ -876,6 +884,8 @@ def vark_paged_attention(q, cu_tokens, k_pages, v_pages, page_table, cache_len, 
               _status_spec(dev_status, torch.int32)]
     dev = q.get_device()
     kp, vp, tp, lp, cp, pq, po, pt, pl, pw, ps = _pointers(dev, specs)
+    if pq == po and n:
+        raise ValueError("out must not overlap q")
     _check(_call_on(dev, stream, _load().vark_paged_attention, dt, pq, _i64_array(q.stride()), n, B, Hq, H, D, cp, kp, vp,
                     n_pages, page_size, tp, max_pages, lp, head_pages, pt, 1 if causal else 0, po,
                     _i64_array(out.stride()), pl, pw, workspace.numel(), ps), "vark_paged_attention")

@@ -76,6 +76,27 @@ int dtype_of(const at::Tensor& t) {
 
 enum Layout { kContiguous, kReadRows, kWrittenRows };
 
+// An output's rows must not overlap: from the smallest stride on, every axis
+// steps over all that the ones before it span.
+bool rows_distinct(const at::Tensor& t) {
+  const int n = int(t.dim()) - 1;
+  int order[8], m = 0;
+  if (n > 8) return false;
+  for (int i = 0; i < n; ++i) {
+    if (t.size(i) <= 1) continue;
+    int at = m++;
+    for (; at > 0 && t.stride(order[at - 1]) > t.stride(i); --at) order[at] = order[at - 1];
+    order[at] = i;
+  }
+  int64_t span = t.size(n);
+  for (int k = 0; k < m; ++k) {
+    const int64_t step = t.stride(order[k]);
+    if (step < span) return false;
+    span += step * (t.size(order[k]) - 1);
+  }
+  return true;
+}
+
 // Pointer of a tensor that has the type, shape, device and layout asked for
 // (null for none).
 template <typename T>
@@ -88,9 +109,7 @@ T* pointer(const at::Tensor* t, at::ScalarType type, int device, std::initialize
     if (layout == kContiguous) throw Unsure{};
     const int n = int(t->dim());
     if (t->stride(n - 1) != 1) throw Unsure{};
-    if (layout == kWrittenRows)      // an output's rows must not overlap
-      for (int i = 0; i + 1 < n; ++i)
-        if (t->size(i) > 1 && t->stride(i) < t->size(n - 1)) throw Unsure{};
+    if (layout == kWrittenRows && !rows_distinct(*t)) throw Unsure{};
   }
   return static_cast<T*>(t->data_ptr());
 }
@@ -255,6 +274,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (H < 1 || Hq % H != 0) throw Unsure{};
     const auto* pq = pointer<uint16_t>(&q, type, dev, {N, Hq, D}, kReadRows);
     auto* po = pointer<uint16_t>(out, type, dev, {N, Hq, D}, kWrittenRows);
+    if (po == pq && po != nullptr) throw Unsure{};
     const Pool p(kp, tensor(a[3]), tab, tensor(a[5]), needed(tensor(a[1])), type, dev, H, D);
     const auto* pt = pointer<float>(tensor(a[6]), at::kFloat, dev, {Hq});
     auto* pl = pointer<float>(tensor(a[9]), at::kFloat, dev, {N, Hq});

@@ -14,6 +14,8 @@
 // log2(D / 16) shuffles.  A warp takes one token and up to 16 heads of it: all
 // rows are loaded first, and the token's cosines and sines are read once for
 // all of them.
+#include <cfloat>
+
 #include "vark_paged.cuh"
 
 namespace vark {
@@ -268,13 +270,21 @@ __global__ void __launch_bounds__(kRowThreads, 12) append_kernel(const __grid_co
     }
   }
   const int b = find_sequence(p.cu, p.B, token, lane);
+  // Offsets that descend or leave the chunk are recorded, 32 a warp.
+  if (blockIdx.y == 0) {
+    for (int64_t e = int64_t(token) * 32 + lane; e < p.B; e += int64_t(p.tokens) * 32) {
+      const int lo = p.cu[e], hi = p.cu[e + 1];
+      if (lo < 0 || hi < lo || hi > p.tokens) record(p.status, VARK_E_SHAPE);
+    }
+  }
   if (b < 0 || b >= p.B || pos == -1) return;   // outside every sequence, or padding
   if (pos == -2) {
     if (lane == 0) record(p.status, VARK_E_SHAPE);
     return;
   }
-  const int first = p.cu[b], n = p.cu[b + 1] - first;
-  if (token - first >= n) return;               // tables that do not ascend
+  const int first = p.cu[b], end = p.cu[b + 1];
+  if (first < 0 || end > p.tokens || token >= end) return;      // offsets outside the chunk, or descending
+  const int n = end - first;
   ln.load(p.rot, pos);
   float wt[16];
   load_weight(p.weight, ln.v, wt);
@@ -284,10 +294,11 @@ __global__ void __launch_bounds__(kRowThreads, 12) append_kernel(const __grid_co
     norm_rotate<DT, D>(kw[r], p.norm, p.eps, p.weight != nullptr, wt, p.rot, ln);
     if (h >= p.pg.heads) continue;
     const int64_t e = int64_t(b) * p.pg.table_heads + (p.pg.table_heads > 1 ? h : 0);
-    const int64_t row = int64_t(p.pg.len[e]) - n + (token - first);
-    if (row < 0) continue;                      // the cache holds only the chunk's last len rows
-    const int64_t pi = row >> p.pg.log2_page;
-    const int64_t page = pi < p.pg.max_pages ? p.pg.table[e * p.pg.max_pages + pi] : -1;
+    const int len = p.pg.len[e];
+    const bool fits = len >= 0 && (len - 1) >> p.pg.log2_page < p.pg.max_pages;
+    const int row = len - n + (token - first);
+    if (fits && row < 0) continue;              // the cache holds only the chunk's last len rows
+    const int64_t page = fits ? p.pg.table[e * p.pg.max_pages + (row >> p.pg.log2_page)] : -1;
     if (page < 0 || page >= p.pg.n_pages) {
       record(p.status, VARK_E_SHAPE);
       continue;
@@ -307,6 +318,7 @@ __global__ void __launch_bounds__(kRowThreads, 12) append_kernel(const __grid_co
 static int check_common(int dtype, int D, int norm, float eps) {
   if (dtype != VARK_BF16 && dtype != VARK_FP16) return VARK_E_ARG;
   if (norm < VARK_NORM_NONE || norm > VARK_NORM_L2 || !(eps >= 0.f)) return VARK_E_ARG;
+  if (norm == VARK_NORM_L2 && eps > 0.f && eps < FLT_MIN) return VARK_E_ARG;      // 1 / eps would overflow
   if (D != 64 && D != 128) return VARK_E_SHAPE;
   return VARK_OK;
 }
@@ -321,6 +333,10 @@ static int make_rotation(Rotation* r, const float* rope, int rope_len, int rope_
   return VARK_OK;
 }
 
+// A tensor that is written over itself keeps its strides.
+static bool in_place_alike(const RowTensor& t) {
+  return t.src != t.dst || (t.ss[0] == t.ds[0] && t.ss[1] == t.ds[1] && t.ss[2] == t.ds[2]);
+}
 
 // Grid of warps over (token, block of heads).
 static dim3 token_grid(int64_t tokens, int head_blocks) {
@@ -341,16 +357,18 @@ extern "C" int vark_qk_norm_rope(int dtype, const uint16_t* q, const int64_t* q_
                                  const float* q_weight, const float* k_weight, float eps, const float* rope,
                                  int rope_len, int rope_dim, int pairs, const int32_t* positions,
                                  int32_t* dev_status, void* stream) {
-  if (!dev_status || (!q && !k)) return VARK_E_ARG;
-  if (q && (!q_strides || !q_out || !q_out_strides)) return VARK_E_ARG;
-  if (k && (!k_strides || !k_out || !k_out_strides)) return VARK_E_ARG;
+  if (!dev_status) return VARK_E_ARG;
   int rc = check_common(dtype, D, norm, eps);
   if (rc) return rc;
-  if (B < 0 || T < 0 || (q && Hq < 1) || (k && Hk < 1)) return VARK_E_SHAPE;
+  if (B < 0 || T < 0) return VARK_E_SHAPE;
+  if (B == 0 || T == 0) return check_device_sm100();       // empty tensors have no addresses to look at
+  if ((!q && !k) || (q && (!q_strides || !q_out || !q_out_strides)) || (k && (!k_strides || !k_out || !k_out_strides)))
+    return VARK_E_ARG;
+  if ((q && Hq < 1) || (k && Hk < 1)) return VARK_E_SHAPE;
   if (Hq > 65536 || Hk > 65536 || int64_t(B) * T > INT32_MAX - kRowThreads) return VARK_E_SHAPE;
   NormRopeParams p;
   if ((rc = make_rotation(&p.rot, rope, rope_len, rope_dim, pairs, positions, D))) return rc;
-  p.T = T > 0 ? T : 1;
+  p.T = T;
   p.tokens = B * T;
   p.norm = norm;
   p.eps = eps;
@@ -360,20 +378,21 @@ extern "C" int vark_qk_norm_rope(int dtype, const uint16_t* q, const int64_t* q_
   if (q) {
     const int64_t n[3] = {B, T, Hq};
     p.t[0] = RowTensor{q, q_out, q_weight, {0, 0, 0}, {0, 0, 0}, Hq};
-    if (!take_strides(p.t[0].ss, q_strides, n, 3) || !take_strides(p.t[0].ds, q_out_strides, n, 3) ||
+    if (!take_strides(p.t[0].ss, q_strides, n, 3, 0) || !take_strides(p.t[0].ds, q_out_strides, n, 3, D) ||
         !aligned16(q) || !aligned16(q_out))
       return VARK_E_ALIGN;
+    if (!in_place_alike(p.t[0])) return VARK_E_ARG;
   }
   if (k) {
     const int64_t n[3] = {B, T, Hk};
     p.t[1] = RowTensor{k, k_out, k_weight, {0, 0, 0}, {0, 0, 0}, Hk};
-    if (!take_strides(p.t[1].ss, k_strides, n, 3) || !take_strides(p.t[1].ds, k_out_strides, n, 3) ||
+    if (!take_strides(p.t[1].ss, k_strides, n, 3, 0) || !take_strides(p.t[1].ds, k_out_strides, n, 3, D) ||
         !aligned16(k) || !aligned16(k_out))
       return VARK_E_ALIGN;
+    if (!in_place_alike(p.t[1])) return VARK_E_ARG;
   }
   if (!aligned16(q_weight) || !aligned16(k_weight) || !aligned16(rope)) return VARK_E_ALIGN;
   if ((rc = check_device_sm100())) return rc;
-  if (p.tokens == 0) return VARK_OK;
   p.q_blocks = blocks_of(p.t[0].heads, kQkHeads);
   const dim3 grid = token_grid(p.tokens, p.q_blocks + blocks_of(p.t[1].heads, kQkHeads));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -391,21 +410,22 @@ extern "C" int vark_paged_append(int dtype, const uint16_t* k, const int64_t* k_
                                  int head_pages, int norm, const float* k_weight, float eps, const float* rope,
                                  int rope_len, int rope_dim, int pairs, const int32_t* positions,
                                  int32_t* dev_status, void* stream) {
-  if (!k || !k_strides || !v || !v_strides || !cu_tokens || !k_pages || !v_pages || !page_table || !cache_len ||
-      !dev_status)
-    return VARK_E_ARG;
+  if (!dev_status) return VARK_E_ARG;
   int rc = check_common(dtype, D, norm, eps);
   if (rc) return rc;
-  if (n_tokens < 0 || n_tokens > INT32_MAX - kRowThreads || B < 0 || B > (1 << 24) || H < 1 || H > 65536) return VARK_E_SHAPE;
+  if (n_tokens < 0 || n_tokens > INT32_MAX - kRowThreads || B < 0 || B > (1 << 24) || H < 1 || H > 65536)
+    return VARK_E_SHAPE;
   AppendParams p;
-  if ((rc = make_rotation(&p.rot, rope, rope_len, rope_dim, pairs, positions, D))) return rc;
   if ((rc = make_pages(&p.pg, page_table, cache_len, n_pages, page_size, max_pages, H, head_pages))) return rc;
+  if (n_tokens == 0 || B == 0) return check_device_sm100();       // empty tensors have no addresses to look at
+  if (!k || !k_strides || !v || !v_strides || !cu_tokens || !k_pages || !v_pages || !page_table || !cache_len)
+    return VARK_E_ARG;
+  if ((rc = make_rotation(&p.rot, rope, rope_len, rope_dim, pairs, positions, D))) return rc;
   const int64_t extent[2] = {n_tokens, H};
-  if (!take_strides(p.ks, k_strides, extent, 2) || !take_strides(p.vs, v_strides, extent, 2) || !aligned16(k) || !aligned16(v) ||
-      !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_weight) || !aligned16(rope))
+  if (!take_strides(p.ks, k_strides, extent, 2, 0) || !take_strides(p.vs, v_strides, extent, 2, 0) || !aligned16(k) ||
+      !aligned16(v) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_weight) || !aligned16(rope))
     return VARK_E_ALIGN;
   if ((rc = check_device_sm100())) return rc;
-  if (n_tokens == 0 || B == 0) return VARK_OK;
   p.k = k; p.v = v;
   p.k_pages = k_pages; p.v_pages = v_pages;
   p.cu = cu_tokens;

@@ -81,12 +81,13 @@ struct Pages {
   int table_heads;
 };
 
-// Strides of rows of 16-byte vectors (host): multiples of 8 elements, not
-// negative; the stride of an axis of one entry is not looked at.
-inline bool take_strides(int64_t* to, const int64_t* s, const int64_t* extent, int n) {
+// Strides of rows of 16-byte vectors (host): multiples of 8 elements, at least
+// `least` (0 for rows that are read, D for rows that are written: no two at one
+// address); the stride of an axis of one entry is not looked at.
+inline bool take_strides(int64_t* to, const int64_t* s, const int64_t* extent, int n, int least) {
   for (int i = 0; i < n; ++i) {
     to[i] = extent[i] > 1 ? s[i] : 0;
-    if (to[i] < 0 || to[i] % 8 != 0) return false;
+    if (extent[i] > 1 && (s[i] < least || s[i] % 8 != 0)) return false;
   }
   return true;
 }

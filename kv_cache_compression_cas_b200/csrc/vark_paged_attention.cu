@@ -61,7 +61,7 @@ struct AttnParams {
   float* part_ml;          // [kCtas][2][R][2]
   int32_t* status;
   uint64_t wait_limit_ns;
-  int withhold;            // test hook: slices a warp loads before it stops (-1: all)
+  int withhold;            // test hook: key tiles a CTA loads before it stops (-1: all)
 };
 
 // ------------------------------------------------------------------ the plan
@@ -111,9 +111,9 @@ template <int R, int KT>
 VARK_DEV Entry load_entry(const AttnParams& p, int e) {
   Entry x;
   const int b = p.pg.table_heads > 1 ? p.by_heads(e) : e;
-  x.first = p.cu[b];
-  const int end = p.cu[b + 1];
-  x.len = p.pg.len[e];
+  x.first = __ldcg(p.cu + b);     // (past L1: the join plans before it waits for the kernels ahead of it)
+  const int end = __ldcg(p.cu + b + 1);
+  x.len = __ldcg(p.pg.len + e);
   if (x.first < 0 || end < x.first || end > p.N || x.len < 0 || (x.len - 1) >> p.pg.log2_page >= p.pg.max_pages) {
     record(p.status, VARK_E_SHAPE);
     x.first = x.n = x.len = 0;
@@ -521,7 +521,6 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
   };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  grid_release();
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kSlots; ++i) {
       mbar_init(bar(L::kFull + i), 1);
@@ -541,6 +540,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     tma_prefetch_desc(&tm_v);
   }
   grid_wait();
+  grid_release();           // only now: the join plans before it waits, so what wrote the tables has ended
   const Share share = find_share<kTileR, kTileKT, kTileThreads, false>(p, blockIdx.x);   // syncs the block
   if (share.u0 == share.u1) return;
   if (warp == 1) {
@@ -987,7 +987,6 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   const int warp = int(threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
   const int tid = int(threadIdx.x) - 128;
 
-  grid_release();
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kSlots; ++i) {
       mbar_init(bar(L::kFull + i), 1);
@@ -999,6 +998,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     tma_prefetch_desc(&tm_v);
   }
   grid_wait();
+  grid_release();           // only now: the join plans before it waits, so what wrote the tables has ended
   const Share share = find_share<L::kR, kTileKT, kRowThreads, false>(p, blockIdx.x);   // syncs the block
   if (share.u0 == share.u1) return;
   if (warp < 0) {
@@ -1497,6 +1497,14 @@ static int launch(int D, int rows, const CUtensorMap& k, const CUtensorMap& v, c
   return D == 128 ? launch_rows<DT, 128, 1>(k, v, p, st) : launch_rows<DT, 64, 1>(k, v, p, st);
 }
 
+// Rows of the call are counted in 30 bits, entries of the length table in 24.
+static int check_shapes(int64_t n_tokens, int B, int Hq, int Hkv, int D) {
+  if (D != 64 && D != 128) return VARK_E_SHAPE;
+  if (n_tokens < 0 || B < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq > 65536) return VARK_E_SHAPE;
+  if (n_tokens > INT32_MAX / 2 / Hq || int64_t(B) * Hkv > (1 << 24)) return VARK_E_SHAPE;
+  return VARK_OK;
+}
+
 static int64_t workspace_bytes_for(int rows, int D) { return int64_t(kCtas) * 2 * rows * (D + 2) * 4; }
 
 }  // namespace paged
@@ -1507,9 +1515,8 @@ using namespace vark::paged;
 
 extern "C" int64_t vark_paged_attention_workspace(int64_t n_tokens, int B, int Hq, int Hkv, int D, int page_size,
                                                   int max_pages) {
-  if (D != 64 && D != 128) return VARK_E_SHAPE;
-  if (n_tokens < 0 || B < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || page_size < 1 || max_pages < 1)
-    return VARK_E_SHAPE;
+  if (const int rc = check_shapes(n_tokens, B, Hq, Hkv, D)) return rc;
+  if (page_size < 1 || max_pages < 1) return VARK_E_SHAPE;
   return workspace_bytes_for(choose_rows(n_tokens, B, Hq, Hkv, D), D);
 }
 
@@ -1520,24 +1527,23 @@ extern "C" int vark_paged_attention(int dtype, const uint16_t* q, const int64_t*
                                     int head_pages, const float* tau, int causal, uint16_t* out,
                                     const int64_t* out_strides, float* lse, void* workspace, int64_t workspace_bytes,
                                     int32_t* dev_status, void* stream) {
-  if (!q || !q_strides || !cu_tokens || !k_pages || !v_pages || !page_table || !cache_len || !out || !out_strides ||
-      !workspace || !dev_status)
-    return VARK_E_ARG;
-  if (dtype != VARK_BF16 && dtype != VARK_FP16) return VARK_E_ARG;
-  if (D != 64 && D != 128) return VARK_E_SHAPE;
-  if (n_tokens < 0 || B < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq > 65536) return VARK_E_SHAPE;
-  if (n_tokens * Hq > INT32_MAX / 2 || int64_t(B) * Hkv > (1 << 24)) return VARK_E_SHAPE;
-  AttnParams p;
-  int rc = make_pages(&p.pg, page_table, cache_len, n_pages, page_size, max_pages, Hkv, head_pages);
+  if (!dev_status || (dtype != VARK_BF16 && dtype != VARK_FP16)) return VARK_E_ARG;
+  int rc = check_shapes(n_tokens, B, Hq, Hkv, D);
   if (rc) return rc;
+  AttnParams p;
+  if ((rc = make_pages(&p.pg, page_table, cache_len, n_pages, page_size, max_pages, Hkv, head_pages))) return rc;
+  if (n_tokens == 0 || B == 0) return check_device_sm100();       // empty tensors have no addresses to look at
+  if (!q || !q_strides || !cu_tokens || !k_pages || !v_pages || !page_table || !cache_len || !out || !out_strides ||
+      !workspace)
+    return VARK_E_ARG;
   if (workspace_bytes < vark_paged_attention_workspace(n_tokens, B, Hq, Hkv, D, page_size, max_pages))
     return VARK_E_ARG;
   const int64_t extent[2] = {n_tokens, Hq};
-  if (!take_strides(p.qs, q_strides, extent, 2) || !take_strides(p.os, out_strides, extent, 2)) return VARK_E_ALIGN;
+  if (!take_strides(p.qs, q_strides, extent, 2, 0) || !take_strides(p.os, out_strides, extent, 2, D))
+    return VARK_E_ALIGN;
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned16(workspace))
     return VARK_E_ALIGN;
   if ((rc = check_device_sm100())) return rc;
-  if (n_tokens == 0 || B == 0) return VARK_OK;
   p.q = q; p.out = out; p.lse = lse;
   p.cu = cu_tokens;
   p.tau = tau;

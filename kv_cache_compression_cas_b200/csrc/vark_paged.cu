@@ -24,10 +24,9 @@ namespace paged {
 // Both kernels are bound by HBM at large sizes and by one chain of dependent
 // loads (position -> cosines) at small ones: the position is asked for before
 // the rows, rows are read and written as streams, and blocks are small so that
-// a finished one makes room at once.  Last scale of a batch of 8, 32768 tokens
-// of 16 + 16 heads: 95 us (5.65 TB/s); 128-thread blocks 102, the position
-// after the rows 111 with plain stores, 8 heads a warp 105, 6 blocks of 128 at
-// 80 registers 101.
+// a finished one makes room at once.  Measured on the last scale of a batch of
+// 8 (32768 tokens of 16 + 16 heads of 128): 92 us, 5.83 TB/s; 128-thread blocks
+// 100, the position after the rows 111 with plain stores, 8 heads a warp 105.
 constexpr int kRowThreads = 64;
 
 struct Rotation {
@@ -159,8 +158,12 @@ struct NormRopeParams {
 
 constexpr int kQkHeads = 16;       // heads of a warp's token
 
+// Blocks an SM, that is registers: 128 channels 10 blocks of 96 (above: 92 us;
+// 12 of 80 spill: 100), 64 channels, which hold half as many rows, 14 of 72
+// (8191 tokens of 32 + 8 heads out of a fused projection: 20.4 us, 4.1 TB/s;
+// 12 of 80 21.5, 10 of 95 24.3).
 template <int DT, int D>
-__global__ void __launch_bounds__(kRowThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kRowThreads, D == 64 ? 14 : 10) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int kLanes = D / 16, kRows = 32 / kLanes, kIters = kQkHeads / kRows;
   const int lane = threadIdx.x & 31, li = lane % kLanes;
   const int token = int(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
@@ -238,8 +241,9 @@ VARK_DEV int find_sequence(const int32_t* cu, int B, int64_t token, int lane) {
 
 constexpr int kKvHeads = 8;        // heads of a warp's token
 
-// 12 blocks an SM (80 registers): 47.8 us for 4 x 4096 tokens of 16 heads into
-// head pages (5.6 TB/s); unbounded (91 registers) 49.3, 4 heads a warp 51.4.
+// 12 blocks an SM (80 registers): 46.1 us for 4 x 4096 tokens of 16 heads into
+// head pages (5.8 TB/s); unbounded (91 registers) 47.5, 4 heads a warp 50.  L2
+// prefetches ahead of the wait: 51 (ragged chunks of 79 MB 15.6 instead of 16.5).
 template <int DT, int D>
 __global__ void __launch_bounds__(kRowThreads, 12) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kLanes = D / 16, kRows = 32 / kLanes, kIters = (kKvHeads + kRows - 1) / kRows;

@@ -614,7 +614,6 @@ def _i64_array(values):
     return (_I64 * len(values))(*values)
 
 
-
 def _paged_dtype(t, name):
     torch = _torch()
     if t.dtype is torch.bfloat16:
@@ -844,8 +843,8 @@ def vark_paged_append(k, v, cu_tokens, k_pages, v_pages, page_table, cache_len, 
               _status_spec(dev_status, torch.int32)]
     dev = k.get_device()
     kp, vp, tp, lp, cp, pk, pv, pw, pr, pp, ps = _pointers(dev, specs)
-    _check(_call_on(dev, stream, _load().vark_paged_append, dt, pk, _i64_array(k.stride()), pv, _i64_array(v.stride()), n, B,
-                    H, D, cp, kp, vp, n_pages, page_size, tp, max_pages, lp, head_pages, norm, pw, eps, pr, rope_len,
+    _check(_call_on(dev, stream, _load().vark_paged_append, dt, pk, _i64_array(k.stride()), pv,
+                    _i64_array(v.stride()), n, B, H, D, cp, kp, vp, n_pages, page_size, tp, max_pages, lp, head_pages, norm, pw, eps, pr, rope_len,
                     rope_dim, 1 if pairs else 0, pp, ps), "vark_paged_append")
 
 
@@ -886,6 +885,6 @@ def vark_paged_attention(q, cu_tokens, k_pages, v_pages, page_table, cache_len, 
     kp, vp, tp, lp, cp, pq, po, pt, pl, pw, ps = _pointers(dev, specs)
     if pq == po and n:
         raise ValueError("out must not overlap q")
-    _check(_call_on(dev, stream, _load().vark_paged_attention, dt, pq, _i64_array(q.stride()), n, B, Hq, H, D, cp, kp, vp,
-                    n_pages, page_size, tp, max_pages, lp, head_pages, pt, 1 if causal else 0, po,
+    _check(_call_on(dev, stream, _load().vark_paged_attention, dt, pq, _i64_array(q.stride()), n, B, Hq, H, D, cp, kp,
+                    vp, n_pages, page_size, tp, max_pages, lp, head_pages, pt, 1 if causal else 0, po,
                     _i64_array(out.stride()), pl, pw, workspace.numel(), ps), "vark_paged_attention")

@@ -163,7 +163,8 @@ constexpr int kQkHeads = 16;       // heads of a warp's token
 // (8191 tokens of 32 + 8 heads out of a fused projection: 20.4 us, 4.1 TB/s;
 // 12 of 80 21.5, 10 of 95 24.3).
 template <int DT, int D>
-__global__ void __launch_bounds__(kRowThreads, D == 64 ? 14 : 10) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kRowThreads, D == 64 ? 14 : 10)
+norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int kLanes = D / 16, kRows = 32 / kLanes, kIters = kQkHeads / kRows;
   const int lane = threadIdx.x & 31, li = lane % kLanes;
   const int token = int(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);

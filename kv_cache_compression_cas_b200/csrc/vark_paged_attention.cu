@@ -7,9 +7,9 @@
 // The G query heads of a kv head share its keys, so the G * n rows of a
 // sequence's n tokens (token-major: row = token * G + head) are cut into tiles
 // of R rows: an item is (sequence, kv head, row tile).  Work is split along the
-// keys as well: all items' key tiles are laid end to end and every CTA takes an
-// equal share of them, so one long cache spreads over the whole device and a
-// ragged batch leaves no CTA with the longest sequence.  An item that falls
+// keys as well: all items are laid end to end, each as long as it costs, and
+// every CTA takes an equal share of the whole, so one long cache spreads over
+// the device and a ragged batch leaves no CTA with the longest sequence.  An item that falls
 // into several shares leaves one partial (o, m, l) per CTA in the workspace; a
 // second, small kernel joins them.  Lengths live on the device: every CTA
 // finds its share with one scan over the sequence table.
@@ -55,7 +55,6 @@ struct AttnParams {
   FastDiv by_group, by_heads;   // / G, / kv heads
   int tokens_per_tile;     // R / G
   int tile_step;           // kUnit R / G: weight from a row tile to the next under a causal mask
-  int item_cost;           // key tiles that an item counts for besides its own
   float scale_log2;        // log2(e) / sqrt(D)
   float* part_o;           // [kCtas][2][R][D]
   float* part_ml;          // [kCtas][2][R][2]
@@ -67,12 +66,16 @@ struct AttnParams {
 // ------------------------------------------------------------------ the plan
 // An entry is one row of the length table: a sequence (shared pages, all kv
 // heads) or a (sequence, head).  Its items, head after head and row tile after
-// row tile, weigh what they cost, in sixteenths of a key: item_cost tiles for
+// row tile, weigh what they cost, in sixteenths of a key: kItemCost tiles for
 // starting and finishing one, and the keys its rows see -- which under a causal
 // mask grow by the tokens of a tile from one row tile to the next, so the
 // weights and their sums have a closed form.  (Equal weights left causal
 // prompts with shares of 0.6 to 1.5 times the mean work.)
 constexpr int kUnit = 16;
+// Key tiles that an item counts for besides its own.  Of 0 / 1 / 2 / 3 / 5: 64
+// sequences decoding 202 / 190 / 190 / 192 / 196 us, drafted tokens of 64
+// channels 69 / 51 / 47 / 47 / 49, prompts 645 / 516 / 458 / 455 / 483.
+constexpr int kItemCost = 2;
 // a / b of non-negative numbers, in 32 bits where they allow it (64 take ten
 // times as long).
 VARK_DEV int64_t quotient(int64_t a, int64_t b) {
@@ -124,7 +127,7 @@ VARK_DEV Entry load_entry(const AttnParams& p, int e) {
   x.heads = p.pg.table_heads > 1 ? 1 : p.pg.heads;
   x.slope = p.causal && x.row_tiles > 1 ? p.tile_step : 0;
   const int seen0 = x.slope ? min(x.len, max(0, x.len - x.n) + p.tokens_per_tile) : x.len;     // by the first row tile
-  x.weight0 = int64_t(kUnit) * (int64_t(p.item_cost) * KT + seen0);
+  x.weight0 = int64_t(kUnit) * (int64_t(kItemCost) * KT + seen0);
   return x;
 }
 
@@ -136,7 +139,7 @@ struct ItemPlace {
   template <int KT>
   VARK_DEV int tile_at(const AttnParams& p, int64_t u) const {
     if (u >= to) return key_tiles;
-    const int64_t k = (u - from) / (kUnit * KT) - p.item_cost;
+    const int64_t k = (u - from) / (kUnit * KT) - kItemCost;
     return int(max(int64_t(0), min(int64_t(key_tiles), k)));
   }
 };
@@ -329,6 +332,17 @@ VARK_DEV void store_row8(const AttnParams& p, const RowAt& a, int d0, const floa
 // memory and is rescaled only when a row's maximum grows by more than 2^8.
 // The MMA warp runs its loop with all lanes and only predicates the MMAs:
 // descriptors and addresses then stay warp-uniform.
+//
+// Measured (32 heads of 128 over 8 kv heads, bf16): a chunk of 2048 tokens over
+// 16384 cached rows 498 us, 1.17 PFLOP/s, while the clock holds, 567 us (1.03)
+// call after call at the power limit; 8 prompts of 333 to 4099 tokens 443 to
+// 499 us.  A pair of tiles takes 3500 cycles for 128 keys: 2050 of MMAs, whose
+// S products read 128 B/clk of shared memory, and as much of exp2 on the two
+// softmax warps of an SM quarter.  What ties them is S -> softmax -> PV -> S.
+// Keys in halves with S a half ahead cut that chain and cost 535 and 495 us:
+// N = 64 products read 192 B/clk, and barriers come twice as often.  P in two
+// chunks 556 for 521, a share of the exponentials as polynomials 4 to 10% more.
+// An item costs 10000 cycles besides its key tiles: prompts feel it.
 // TMEM: S_A [0,128) S_B [128,256) O_A [256,256+D) O_B [256+D,256+2D).
 constexpr int kTileThreads = 384;
 constexpr int kTileR = 256;
@@ -910,6 +924,14 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
 // barrier among them until an item ends, when their results are added in
 // shared memory.  The products run on mma.sync: 16 rows fill its tile where a
 // tcgen05 tile would be one eighth full.
+//
+// Measured (32 heads of 128 over 8 kv heads, bf16): 64 sequences of up to 8190
+// rows out of 16-row pages 191 us with its join, 6.3 TB/s; one of 65536 rows
+// 49 us, 5.5 TB/s, of which 7 are finding the share, the handoff and the join.
+// 3 to 7 drafted tokens of 24 heads of 64 for each of 32 caches of up to 4000 rows
+// 46 us, 3.2 TB/s: a segment of 30 tiles pays 3 tiles' time to start and end,
+// and a tile's chain (ldmatrix, MMAs, maximum, exp2, MMAs) is not covered by a
+// second one in the warp.
 // (Warps 0-3 are the loader's group; three of them only hand their registers on.)
 constexpr int kRowWarps = 8;
 constexpr int kRowThreads = kRowWarps * 32 + 128;
@@ -1287,8 +1309,9 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
 // most two such items, at its two ends: one for each half of its threads.
 // Threads that a few pieces would leave idle share the parts of one.  All that
 // does not need the partials is done before the attention ends; the CTA waits
-// beside a running rows kernel, in the registers that leaves.  (One CTA per
-// item took 5 us for 19 parts, a row a CTA 4.)
+// beside a running rows kernel, in the registers that leaves.  Bound by two
+// dependent loads after the handoff, 2 to 3 us.  (One CTA per item took 5 us for
+// 19 parts, a row a CTA 4.)
 template <int R>
 struct JoinShape { static constexpr int kHalf = 128, kSplit = R == kTileR ? 4 : 1; };
 
@@ -1553,7 +1576,6 @@ extern "C" int vark_paged_attention(int dtype, const uint16_t* q, const int64_t*
   p.by_heads = FastDiv::of(Hkv);
   p.scale_log2 = kLog2e / sqrtf(float(D));
   const int rows = choose_rows(n_tokens, B, Hq, Hkv, D);
-  p.item_cost = rows == kTileR || D == 64 ? 3 : 1;   // measured best of 0 (1) to 4
   p.tokens_per_tile = rows / p.G;
   p.tile_step = rows * kUnit / p.G;
   p.part_ml = static_cast<float*>(workspace);

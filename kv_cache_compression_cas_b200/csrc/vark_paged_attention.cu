@@ -929,9 +929,9 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
 // rows out of 16-row pages 191 us with its join, 6.3 TB/s; one of 65536 rows
 // 49 us, 5.5 TB/s, of which 7 are finding the share, the handoff and the join.
 // 3 to 7 drafted tokens of 24 heads of 64 for each of 32 caches of up to 4000 rows
-// 46 us, 3.2 TB/s: a segment of 30 tiles pays 3 tiles' time to start and end,
-// and a tile's chain (ldmatrix, MMAs, maximum, exp2, MMAs) is not covered by a
-// second one in the warp.
+// 46 us, 3.2 TB/s: an item of some 16 key tiles pays 2 tiles' time to start and
+// end, and a tile's chain (ldmatrix, MMAs, maximum, exp2, MMAs) is not covered
+// by a second one in the warp.
 // (Warps 0-3 are the loader's group; three of them only hand their registers on.)
 constexpr int kRowWarps = 8;
 constexpr int kRowThreads = kRowWarps * 32 + 128;

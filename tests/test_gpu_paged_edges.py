@@ -43,6 +43,74 @@ def test_paged_attention_edges(dtype, case):
     compare(pg, q, tau, causal, out, lse, dtype)
 
 
+MANY = [
+    # n, lens, Hq, H, D, page, head_pages: more sequences (and heads) than a block has threads
+    ([i % 3 for i in range(900)], [1 + (i * 7) % 40 for i in range(900)], 2, 2, 64, 16, False),
+    ([1] * 70, [[(b * 11 + h * 5) % 33 for h in range(9)] for b in range(70)], 9, 9, 64, 16, True),
+    ([20] * 60, [[20 + (b + h) % 50 for h in range(12)] for b in range(60)], 24, 12, 64, 32, True),
+    ([1], [3], 5000, 5000, 64, 16, False),
+]
+
+
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_many_sequences_and_heads(case):
+    n, lens, Hq, H, D, page, head = MANY[case]
+    rng = np.random.default_rng(700 + case)
+    pg = Pages(rng, "bf16", n, lens, H, D, page, head)
+    N = int(pg.cu[-1])
+    q = rounded(rng.standard_normal((N, Hq, D)), "bf16")
+    out, lse = run_attention(pg, q, None, True)
+    compare(pg, q, None, True, out, lse, "bf16")
+    d = pg.cuda()
+    k, v = (rounded(rng.standard_normal((N, H, D)), "bf16").cuda() for _ in range(2))
+    want = [d["k_pages"].clone(), d["v_pages"].clone()]
+    for b in range(len(n)):
+        for i in range(n[b]):
+            for h in range(H if head else 1):
+                at = ref.paged_row(pg.table, pg.lens, pg.cu, page, b, h, i)
+                if at is None:
+                    continue
+                t = int(pg.cu[b]) + i
+                for to, x in zip(want, (k, v)):
+                    if head:
+                        to[at] = x[t, h]
+                    else:
+                        to[at[0], :, at[1]] = x[t]
+    st = status_word()
+    vark.vark_paged_append(k, v, d["cu_tokens"], d["k_pages"], d["v_pages"], d["page_table"], d["cache_len"],
+                           vark.VARK_NORM_NONE, None, 0.0, None, None, st)
+    check_status(st)
+    assert same_bits(d["k_pages"], want[0]) and same_bits(d["v_pages"], want[1])
+
+
+def test_broadcast_rows_are_read():
+    """Strides of 0: one row for all heads, one token for all sequences."""
+    rng = np.random.default_rng(3)
+    pg = Pages(rng, "bf16", [2, 3], [40, 9], 4, 128, 16, False)
+    one = rounded(rng.standard_normal((5, 1, 128)), "bf16").cuda()
+    st = status_word()
+    pools = []
+    for k in (one.expand(5, 4, 128), one.expand(5, 4, 128).contiguous()):
+        d = pg.cuda()
+        vark.vark_paged_append(k, k, d["cu_tokens"], d["k_pages"], d["v_pages"], d["page_table"], d["cache_len"],
+                               vark.VARK_NORM_RMS, None, 1e-6, None, None, st)
+        pools.append((d["k_pages"], d["v_pages"]))
+    check_status(st)
+    assert same_bits(pools[0][0], pools[1][0]) and same_bits(pools[0][1], pools[1][1])
+    row = rounded(rng.standard_normal((1, 1, 128)), "bf16").cuda()
+    d = pg.cuda()
+    ws = torch.empty(vark.vark_paged_attention_workspace(5, 2, 8, 4, 128, 16, pg.table.shape[-1]), dtype=torch.uint8,
+                     device="cuda")
+    outs = []
+    for q in (row.expand(5, 8, 128), row.expand(5, 8, 128).contiguous()):
+        out = torch.empty(5, 8, 128, dtype=torch.bfloat16, device="cuda")
+        vark.vark_paged_attention(q, d["cu_tokens"], d["k_pages"], d["v_pages"], d["page_table"], d["cache_len"], None,
+                                  True, out, None, ws, st)
+        outs.append(out)
+    check_status(st)
+    assert same_bits(*outs)
+
+
 def test_calls_with_nothing_to_do():
     rng = np.random.default_rng(1)
     bf, i32 = torch.bfloat16, torch.int32

@@ -1310,8 +1310,9 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
 // Threads that a few pieces would leave idle share the parts of one.  All that
 // does not need the partials is done before the attention ends; the CTA waits
 // beside a running rows kernel, in the registers that leaves.  Bound by two
-// dependent loads after the handoff, 2 to 3 us.  (One CTA per item took 5 us for
-// 19 parts, a row a CTA 4.)
+// dependent loads after the handoff, 2 to 3 us for few rows, and by reading the
+// partials out of L2 for many.  (One CTA per item took 5 us for 19 parts, a row a
+// CTA 4; finding the parts again for every piece 1 to 3 more.)
 template <int R>
 struct JoinShape { static constexpr int kHalf = 128, kSplit = R == kTileR ? 4 : 1; };
 
@@ -1322,21 +1323,20 @@ __global__ void __launch_bounds__(2 * JoinShape<R>::kHalf, 4) join_kernel(const 
   constexpr int kSlots = kHalf / 4;             // (piece, part) slots of 4 threads, 8 channels each
   __shared__ __align__(16) float red_all[2][kSlots][32 + 4];
   __shared__ float red_ml_all[2][kSlots][2];
+  __shared__ int part_all[2][kCtas];            // the first row of a share's part in the workspace, or -1
+  __shared__ int whole[2];                      // one share did all of the item
   const int c = blockIdx.x;
+  if (threadIdx.x < 2) whole[threadIdx.x] = 0;
   grid_release();
   const Share s = find_share<R, KT, 2 * kHalf, true>(p, c);
   const int k = threadIdx.x / kHalf, tid = threadIdx.x % kHalf;
   auto red = red_all[k];
   auto red_ml = red_ml_all[k];
+  auto part_row = part_all[k];
   const int d1 = (tid & 3) * 8, slot = tid >> 2;
   Segments<R, KT> seg;
   ItemPlace item = {0, 0, 0};
   int c0 = 0, n = 0;                            // the shares that may hold a part
-  // Share c0 + q's key tiles [k0, k1) of the item; none where k0 == k1.
-  auto part = [&](int q, int& k0, int& k1) {
-    k0 = item.tile_at<KT>(p, max(item.from, s.begin(c0 + q)));
-    k1 = item.tile_at<KT>(p, min(item.to, s.begin(c0 + q + 1)));
-  };
   bool work = s.u0 != s.u1;
   if (work) {
     const Share::Place& at = k ? s.last : s.first;
@@ -1350,13 +1350,15 @@ __global__ void __launch_bounds__(2 * JoinShape<R>::kHalf, 4) join_kernel(const 
   if (work) {
     c0 = s.holder(item.from);
     n = s.holder(item.to - 1) - c0 + 1;
-    for (int q = 0; q < n; ++q) {
-      int k0, k1;
-      part(q, k0, k1);
-      if (k0 == 0 && k1 == item.key_tiles) work = false;                 // one share did it all
-      if (k1 > 0) break;
+    for (int q = tid; q < n; q += kHalf) {       // share c0 + q's key tiles [k0, k1) of the item
+      const int k0 = item.tile_at<KT>(p, max(item.from, s.begin(c0 + q)));
+      const int k1 = item.tile_at<KT>(p, min(item.to, s.begin(c0 + q + 1)));
+      part_row[q] = k0 < k1 ? ((c0 + q) * 2 + (k0 == 0 ? 1 : 0)) * R : -1;
+      if (k0 == 0 && k1 == item.key_tiles) whole[k] = 1;
     }
   }
+  __syncthreads();
+  work = work && !whole[k];
   const int pieces = work ? min(R, seg.x.n * p.G - seg.tile * R) * kPieces : 0;
   const int first = c - c0 + int(blockIdx.y) * n, step = n * int(gridDim.y);
   const int mine = work ? (pieces - first + step - 1) / step : 0;
@@ -1384,10 +1386,9 @@ __global__ void __launch_bounds__(2 * JoinShape<R>::kHalf, 4) join_kernel(const 
           const int q = q0 + b * parts;
           v[b] = make_float2(-INFINITY, 0.f);
           w[b][0] = w[b][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-          int k0 = 0, k1 = 0;
-          if (q < n) part(q, k0, k1);
-          if (k0 < k1) {
-            const int64_t from = (int64_t(c0 + q) * 2 + (k0 == 0 ? 1 : 0)) * R + r;
+          const int row = q < n ? part_row[q] : -1;
+          if (row >= 0) {
+            const int64_t from = row + r;
             v[b] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + from * 2));
             w[b][0] = __ldcg(reinterpret_cast<const float4*>(p.part_o + from * D + d0));
             w[b][1] = __ldcg(reinterpret_cast<const float4*>(p.part_o + from * D + d0 + 4));

@@ -9,7 +9,8 @@
 // of R rows: an item is (sequence, kv head, row tile).  Work is split along the
 // keys as well: all items are laid end to end, each as long as it costs, and
 // every CTA takes an equal share of the whole, so one long cache spreads over
-// the device and a ragged batch leaves no CTA with the longest sequence.  An item that falls
+// the device and a ragged batch leaves no CTA with the longest sequence (a few
+// short items of many rows stay whole: kCutTiles).  An item that falls
 // into several shares leaves one partial (o, m, l) per CTA in the workspace; a
 // second, small kernel joins them.  Lengths live on the device: every CTA
 // finds its share with one scan over the sequence table.
@@ -22,6 +23,7 @@ namespace vark {
 namespace paged {
 
 constexpr int kCtas = 148;             // one persistent CTA per SM
+constexpr int kTileR = 256;            // rows of an item of the tiles kernel
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;       // log2: a running maximum may lag by this much
@@ -76,6 +78,11 @@ constexpr int kUnit = 16;
 // sequences decoding 202 / 190 / 190 / 192 / 196 us, drafted tokens of 64
 // channels 69 / 51 / 47 / 47 / 49, prompts 645 / 516 / 458 / 455 / 483.
 constexpr int kItemCost = 2;
+// Where there is a CTA for every item of 256 rows, cutting one up must save more
+// than this many key tiles' time, which its partial results and the join cost:
+// 200 tokens over 16 rows (32 heads of 128) 25.2 -> 19.4 us whole, 8 times 100
+// over 1000 46.5 -> 35.9; at 9 one chunk of 64 over 700 loses 22.8 -> 25.1.
+constexpr int kCutTiles = 6;
 // a / b of non-negative numbers, in 32 bits where they allow it (64 take ten
 // times as long).
 VARK_DEV int64_t quotient(int64_t a, int64_t b) {
@@ -91,6 +98,11 @@ struct Entry {
   VARK_DEV int64_t sum(int t) const { return t * weight0 + int64_t(slope) * t * (t - 1) / 2; }   // of tiles 0 .. t-1
   VARK_DEV int64_t head_units() const { return sum(row_tiles); }
   VARK_DEV int64_t units() const { return heads * head_units(); }
+  VARK_DEV int64_t longest() const { return row_tiles == 0 ? 0 : weight0 + int64_t(row_tiles - 1) * slope; }
+  VARK_DEV void count_items() {                // every item weighs one unit
+    slope = 0;
+    weight0 = 1;
+  }
   // The row tile that holds unit `off` of a head.
   VARK_DEV int tile_of(int64_t off) const {
     int t;
@@ -162,36 +174,80 @@ struct Share {
   }
 };
 
+// Running sum over the lanes of a warp.
+template <typename T>
+VARK_DEV T lane_sums(T v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+// From the warps' sums: what lies before this warp, and all of it.  (By lanes:
+// a loop over the warps, unrolled, is 100 instructions that run once, and those
+// cost most by being fetched.)
+template <int WARPS, typename T>
+VARK_DEV void warp_sums(const T* of, int warp, int lane, T& before, T& total) {
+  const T own = lane < WARPS ? of[lane] : T(0);
+  const T incl = lane_sums(own, lane);
+  total = __shfl_sync(0xffffffffu, incl, WARPS - 1);
+  before = __shfl_sync(0xffffffffu, incl - own, warp);
+}
+
 // Scan over the entries by the whole block: the share of CTA `cta`, and where
 // its first unit (and with LAST its last one) lies.
 template <int R, int KT, int THREADS, bool LAST>
 VARK_DEV Share find_share(const AttnParams& p, int cta) {
-  __shared__ int64_t warp_sum[THREADS / 32];
+  constexpr int kWarps = THREADS / 32;
+  constexpr int64_t kTile = int64_t(kUnit) * KT;
+  constexpr bool kMayCount = R == kTileR;
+  __shared__ int64_t warp_sum[kWarps];
+  __shared__ int warp_longest[kWarps], warp_items[kWarps];
   __shared__ Share::Place found[2];
   const int E = p.B * p.pg.table_heads;
   const int chunk = (E + THREADS - 1) / THREADS;
   const int e0 = min(E, int(threadIdx.x) * chunk), e1 = min(E, e0 + chunk);
-  int64_t sum = 0;
+  int64_t sum = 0, items = 0, longest = 0;
   Entry x = {};
   for (int e = e0; e < e1; ++e) {
     x = load_entry<R, KT>(p, e);
     sum += x.units();
+    if (kMayCount) {
+      items += int64_t(x.heads) * x.row_tiles;
+      longest = max(longest, x.longest());
+    }
   }
-  int64_t incl = sum;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+  int64_t incl = lane_sums(sum, lane);
+  if (kMayCount) {
+    const int tiles = __reduce_max_sync(0xffffffffu, int((longest + kTile - 1) / kTile));
+    if (lane == 0) warp_longest[warp] = tiles;
   }
   if (lane == 31) warp_sum[warp] = incl;
   __syncthreads();
   Share s;
-  int64_t before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < warp) before += warp_sum[w];
-    total += warp_sum[w];
+  int64_t before, total;
+  warp_sums<kWarps>(warp_sum, warp, lane, before, total);
+  bool one_each = false;             // every item weighs one unit: none is cut
+  if (kMayCount) {
+    const int tiles = __reduce_max_sync(0xffffffffu, lane < kWarps ? warp_longest[lane] : 0);
+    if ((tiles - kCutTiles) * (kTile * kCtas) <= total) {        // (the same for every thread)
+      const int own = int(min(items, int64_t(kCtas + 1)));
+      const int incl_items = lane_sums(own, lane);
+      if (lane == 31) warp_items[warp] = incl_items;
+      __syncthreads();
+      int before_items, all_items;
+      warp_sums<kWarps>(warp_items, warp, lane, before_items, all_items);
+      if (all_items <= kCtas) {
+        one_each = true;
+        total = all_items;
+        before = before_items;
+        sum = own;
+        incl = incl_items;
+        x.count_items();
+      }
+    }
   }
   s.ctas = int(min(int64_t(kCtas), total));
   s.per = 1;
@@ -211,7 +267,10 @@ VARK_DEV Share find_share(const AttnParams& p, int cta) {
     if (want < from || want >= from + sum) continue;
     int64_t base = from;
     for (int e = e0; e < e1; ++e) {
-      if (chunk > 1) x = load_entry<R, KT>(p, e);     // (else it is the one just read)
+      if (chunk > 1) {                                // (else it is the one just read)
+        x = load_entry<R, KT>(p, e);
+        if (one_each) x.count_items();
+      }
       const int64_t w = x.units();
       if (want < base + w) {
         found[k] = Share::Place{e, base, x};
@@ -270,8 +329,10 @@ struct Segments {
       tile = 0;
       if (++i == x.heads) {
         i = 0;
+        const bool items = R == kTileR && x.weight0 == 1;      // (see count_items)
         do x = load_entry<R, KT>(p, ++e);
         while (x.row_tiles == 0);
+        if (items) x.count_items();
       }
     }
     place(p);
@@ -345,7 +406,6 @@ VARK_DEV void store_row8(const AttnParams& p, const RowAt& a, int d0, const floa
 // An item costs 10000 cycles besides its key tiles: prompts feel it.
 // TMEM: S_A [0,128) S_B [128,256) O_A [256,256+D) O_B [256+D,256+2D).
 constexpr int kTileThreads = 384;
-constexpr int kTileR = 256;
 constexpr int kTileKT = 128;
 constexpr int kMaxSmem = 232448;
 

@@ -34,8 +34,11 @@ def tile_at(u, frm, to, key_tiles, cost):
     return max(0, min(key_tiles, (u - frm) // (UNIT * KT) - cost))
 
 
-def check(batch, R, G, heads, causal, cost):
+def check(batch, R, G, heads, causal, cost, one_each=False):
     items = items_of(batch, R, G, heads, causal, cost)
+    if one_each:                          # no more items than CTAs: every one weighs one unit
+        assert len(items) <= CTAS
+        items = [(1, kt) for _, kt in items]
     starts = [0]
     for w, _ in items:
         assert w > 0
@@ -118,3 +121,15 @@ def test_smallest_and_single_items():
     check([(1, 1 << 20)], 16, 4, 1, True, 3)
     check([(4096, 4096)], 256, 1, 1, False, 3)
     check([(1, 1)] * 300, 32, 1, 16, False, 1)
+
+
+def test_one_item_a_share():
+    """Few short items are not cut: every share is one of them."""
+    rng = random.Random(7)
+    for _ in range(60):
+        batch = [(n, n + rng.randint(0, 700)) for n in (rng.randint(0, 90) for _ in range(rng.randint(1, 18)))]
+        G, heads, causal = rng.choice([1, 4, 5]), rng.choice([1, 2, 4]), rng.random() < 0.5
+        items = items_of(batch, 256, G, heads, causal, 2)
+        if len(items) <= CTAS:
+            check(batch, 256, G, heads, causal, 2, one_each=True)
+    check([(0, 5), (0, 0)], 256, 4, 8, True, 2, one_each=True)

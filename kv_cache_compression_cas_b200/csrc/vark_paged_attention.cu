@@ -989,9 +989,10 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
 // rows out of 16-row pages 191 us with its join, 6.3 TB/s; one of 65536 rows
 // 49 us, 5.5 TB/s, of which 7 are finding the share, the handoff and the join.
 // 3 to 7 drafted tokens of 24 heads of 64 for each of 32 caches of up to 4000 rows
-// 46 us, 3.2 TB/s: an item of some 16 key tiles pays 2 tiles' time to start and
-// end, and a tile's chain (ldmatrix, MMAs, maximum, exp2, MMAs) is not covered
-// by a second one in the warp.
+// 46 us, 3.2 TB/s: 12 us do not shrink with the caches (plan, first loads, items'
+// starts and ends, join), and 6 or 7 tokens are two row tiles that read the keys
+// twice; each further row costs what 6.2 TB/s take.  Two key tiles at a time in
+// a warp: 49 us.
 // (Warps 0-3 are the loader's group; three of them only hand their registers on.)
 constexpr int kRowWarps = 8;
 constexpr int kRowThreads = kRowWarps * 32 + 128;

@@ -598,7 +598,8 @@ enum vark_norm {
  *                not overlap the inputs.
  *   B, T         >= 0, B * T < 2^31 - 128;  Hq, Hk >= 1, <= 65536;  D 64 or 128.
  *   norm         vark_norm;  eps >= 0 (L2: 0 or a normal number).  A row of
- *                zeros with eps = 0 has no norm and gives NaN.
+ *                zeros with eps = 0 has no norm and gives NaN; a NaN in a row
+ *                makes all of it NaN.
  *   q_weight, k_weight  dev fp32 [D], or NULL for ones.
  *   rope         dev fp32 [rope_len][2][rope_dim / 2]: a position's cosines,
  *                then its sines (any angles: one axis, or the 2-D angles of a

@@ -93,7 +93,8 @@ VARK_DEV void norm_rotate(uint4 (&w)[2], int norm, float eps, bool weighted, con
     float ss = s0 + s1;
 #pragma unroll
     for (int o = D / 32; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float inv = norm == VARK_NORM_RMS ? 1.f / sqrtf(ss * (1.f / D) + eps) : 1.f / fmaxf(sqrtf(ss), eps);
+    const float len = sqrtf(ss);                   // (a NaN stays one: fmaxf would give eps for it)
+    const float inv = norm == VARK_NORM_RMS ? 1.f / sqrtf(ss * (1.f / D) + eps) : 1.f / (len < eps ? eps : len);
 #pragma unroll
     for (int e = 0; e < 16; ++e) x[e] *= inv;
   }

@@ -545,7 +545,8 @@ int vark_pruned_attention_int3(const uint16_t* q, const uint8_t* kq, const uint8
  * Element types: `dtype` is VARK_BF16 or VARK_FP16 for every 16-bit tensor of a
  *   call (raw bits in uint16_t); sums, maxima and norms are fp32 and a value is
  *   rounded once, when it is stored (attention rounds its probabilities to
- *   dtype as well, as the calls above do).
+ *   dtype as well, as the calls above do; an fp16 one is off by half a step or
+ *   by 2^-32 of the row's largest).
  * Chunk: the new tokens of all sequences one behind another; cu_tokens (dev
  *   int32 [B + 1], ascending from 0) gives their bounds, sequence b holding
  *   tokens cu_tokens[b] .. cu_tokens[b + 1] - 1, possibly none.  Tokens of no

@@ -27,6 +27,15 @@ constexpr int kTileR = 256;            // rows of an item of the tiles kernel
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;       // log2: a running maximum may lag by this much
+// log2: how far below a row's maximum its probabilities' reference lies.  They
+// are summed in fp32 and rounded to the cache's type for P V, whose MMAs take 16
+// bits.  bf16 has fp32's range; of fp16, below 2^-14 a step is 2^-24 and below
+// 2^-25 nothing is left, so the reference lies where the largest come to 2^15
+// (with the lag): a probability is then off by 2^-32 of the largest at most,
+// where it was 2^-25, at which 65536 keys 17 below one in the logits came out
+// 44% too heavy and 18 below were lost.
+template <int DT>
+constexpr float kLift = DT == VARK_FP16 ? 7.0f : 0.0f;
 
 // Division by a number the host knows, by a product (a division costs 130
 // cycles of latency, and several lie on the way to a CTA's first load).  Of
@@ -835,9 +844,9 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         m1 = fmax3(m1, sv[126], sv[127]);
         const float m_tile = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * qk2;
         float f = 1.f;
-        if (m_tile > m_used + kRescale || (m_used == -INFINITY && m_tile > -INFINITY)) {
-          f = ex2_approx(m_used - m_tile);
-          m_used = m_tile;
+        if (m_tile > m_used + (kRescale + kLift<DT>) || (m_used == -INFINITY && m_tile > -INFINITY)) {
+          f = ex2_approx(m_used - (m_tile - kLift<DT>));
+          m_used = m_tile - kLift<DT>;
           l_sum *= f;
         }
         if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {   // O_X is stable: S_X(j) came after PV_X(j-1)
@@ -1164,7 +1173,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     more = ahead.next(p);
     if (more) fetch(ahead);
     int lim[MT][2];
-    float scale[MT][2], m[MT][2], top[MT][2], l[MT][2], o[MT][NT][4];   // top: m + the lag it may have
+    float scale[MT][2], m[MT][2], top[MT][2], l[MT][2], o[MT][NT][4];   // m: the reference; top: the maximum + its lag
     uint32_t qa[kQRegs ? MT * KS : 1][4];   // the A operand, where it fits the registers
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -1257,8 +1266,8 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             float v = fmaxf(mx[mt][i], __shfl_xor_sync(0xffffffffu, mx[mt][i], 1));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
             if (v > top[mt][i]) {
-              const float f = ex2_approx(m[mt][i] - v);          // (the first time: 0)
-              m[mt][i] = v;
+              const float f = ex2_approx(m[mt][i] - (v - kLift<DT>));          // (the first time: 0)
+              m[mt][i] = v - kLift<DT>;
               top[mt][i] = v + kRescale;
               l[mt][i] *= f;
 #pragma unroll

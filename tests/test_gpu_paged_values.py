@@ -1,5 +1,6 @@
 """The serving calls at values and sizes where a kernel can lose what the
-definition keeps: NaN and infinities in a norm's rows."""
+definition keeps: NaN and infinities in a norm's rows; caches where one key
+outweighs the others."""
 import numpy as np
 import pytest
 import torch
@@ -7,7 +8,7 @@ import torch
 import kv_cache_compression_cas_b200 as vark
 from oracle import paged as ref
 from tests.helpers import check_status, status_word
-from tests.paged_cases import Pages, norm_bound, rounded, values
+from tests.paged_cases import FP16_TINY, Pages, attention_bounds, norm_bound, rounded, values
 from tests.test_gpu_paged import same_bits
 
 pytestmark = pytest.mark.gpu
@@ -49,3 +50,46 @@ def test_nan_and_infinity_in_a_normed_row(dtype, D, norm):
     assert (np.isnan(values(d["k_pages"][page, :, :T])) == np.isnan(y).transpose(1, 0, 2)).all()
     keys = torch.nan_to_num(d["k_pages"][page, :, :T].transpose(0, 1), nan=1.0)
     assert same_bits(keys, torch.nan_to_num(got[0], nan=1.0))
+
+
+# ------------------------------------------------------------------ attention
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("gap", [17.0, 18.0, 10.0])
+@pytest.mark.parametrize("n,G", [(1, 1), (1, 20), (40, 4)])
+@pytest.mark.parametrize("value", [0.0])
+def test_one_key_outweighs_a_long_cache(dtype, D, gap, n, G, value):
+    """The first of 65536 keys has a logit `gap` above the others, which are
+    alike and whose weights together are felt all the same; its value is 0, so
+    the others make all of the output.  160 sequences over the same pages, so
+    that a CTA has long runs of keys (one is half a cache and more); every
+    kernel: 16, 32 and 256 rows."""
+    rng = np.random.default_rng(int(gap) * 1000 + D + G)
+    B, keys, ps = 160, 65536, 256
+    k = np.zeros((keys // ps, 1, ps, D))
+    k[0, 0, 0] = np.float16(gap / np.sqrt(D))           # with q = 1: D of them / sqrt(D)
+    k = rounded(k, dtype)
+    v = rounded(rng.uniform(0.5, 1.5, (keys // ps, 1, ps, D)), dtype)
+    v[0, 0, 0] = value
+    table = np.arange(keys // ps, dtype=np.int32)[None]
+    lens, cu = np.array([keys], dtype=np.int32), np.array([0, 1], dtype=np.int32)
+    one = np.ones((1, 1, D))
+    o, z, mean_abs, logit_abs = ref.paged_attention(one, cu, values(k), values(v), table, lens, np.ones(1), False)
+    N = B * n
+    out = torch.empty(N, G, D, dtype=k.dtype, device="cuda")
+    lse = torch.empty(N, G, device="cuda")
+    ws = torch.empty(vark.vark_paged_attention_workspace(N, B, G, 1, D, ps, keys // ps), dtype=torch.uint8,
+                     device="cuda")
+    st = status_word()
+    vark.vark_paged_attention(torch.ones(N, G, D, dtype=k.dtype, device="cuda"),
+                              torch.arange(B + 1, dtype=torch.int32, device="cuda") * n, k.cuda(), v.cuda(),
+                              torch.from_numpy(table).cuda().expand(B, keys // ps).contiguous(),
+                              torch.from_numpy(lens).cuda().expand(B).contiguous(), None, False, out, lse, ws, st)
+    check_status(st)
+    b_out, b_lse = attention_bounds(o, z, mean_abs, logit_abs, float(keys), dtype, D)
+    if dtype == "fp16":
+        # the bound allows every probability FP16_TINY of the largest, times 6 for |v|; the
+        # reference 2^7 below the maximum makes it 2^-7 of that, and |v| is at most 1.5
+        b_out += keys * FP16_TINY * (1.5 * 2.0 ** -7 - 6.0)
+    assert (np.abs(values(out) - o[0, 0]) <= b_out[0, 0]).all()
+    assert (np.abs(values(lse) - z[0, 0]) <= b_lse[0, 0]).all()

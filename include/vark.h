@@ -668,6 +668,9 @@ int64_t vark_paged_attention_workspace(int64_t n_tokens, int B, int Hq, int Hkv,
  * Rows behind cache_len may hold anything.  The rows of a cache that some query
  *   of the chunk sees must hold finite values (another query that does not see
  *   a NaN or infinity may still be reached by it).
+ * The tensor cores cut a product off 2^-25 below the sum they add it to: an
+ *   output may lose 1.25 2^-25 of the mean |v| for each of up to 32768 keys (few
+ *   rows a kv head: of an eighth of the keys).
  * Limits: n_tokens * Hq < 2^30, B * Hkv <= 2^24.
  * Errors: VARK_E_ARG, VARK_E_SHAPE, VARK_E_ALIGN, VARK_E_CUDA, VARK_E_DEVICE;
  *   *dev_status as vark_scas_accumulate, and the tables' VARK_E_SHAPE.

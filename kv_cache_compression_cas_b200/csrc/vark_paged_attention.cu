@@ -414,6 +414,16 @@ VARK_DEV void store_row8(const AttnParams& p, const RowAt& a, int d0, const floa
 // chunks 556 for 521, a share of the exponentials as polynomials 4 to 10% more.
 // An item costs 10000 cycles besides its key tiles: prompts feel it.
 // TMEM: S_A [0,128) S_B [128,256) O_A [256,256+D) O_B [256+D,256+2D).
+//
+// An MMA cuts its products off 2^-25 below the sum that it adds them to
+// (measured: a key of 2^-25 of the sum counts in full, one of 2^-26 not at all),
+// so n keys can lose 1.25 n 2^-25 of an output while l keeps them: of 2^20 keys
+// of equal weight 0.6% of it, always towards zero.  Every kSumTiles key tiles
+// the softmax threads therefore add O to an fp32 row in the workspace (the slot
+// of the segment's partial result, which nothing else uses meanwhile) and begin
+// it anew: 0.12% at most, 0.02% at equal weights.  That takes as long as 4 key
+// tiles; every 128 tiles 2.5% of the chunk above.
+constexpr int kSumTiles = 256;
 constexpr int kTileThreads = 384;
 constexpr int kTileKT = 128;
 constexpr int kMaxSmem = 232448;
@@ -802,6 +812,37 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
       w.slot = (int(blockIdx.x) * 2 + (sg.k0 == 0 ? 1 : 0)) * kTileR + x * 128 + r;
       return true;
     };
+    // O and the row in the workspace (see kSumTiles; its reference in part_ml): both
+    // added up in the row (`save`; O is left at 0), or in O.
+    auto move_sum = [&](int slot, float m_used, bool held, bool save) {
+      float4* sum = reinterpret_cast<float4*>(p.part_o + int64_t(slot) * D);
+      const float m_sum = held ? p.part_ml[int64_t(slot) * 2] : -INFINITY;
+      const float g = m_sum == -INFINITY ? 0.f : ex2_approx(m_sum - m_used);
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t v[32];
+        tmem_ld32(tO + c * 32, v);
+        tmem_wait_ld();
+        reg_fence32(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (held) a = sum[c * 8 + i];
+          a.x = fmaf(a.x, g, __uint_as_float(v[4 * i]));
+          a.y = fmaf(a.y, g, __uint_as_float(v[4 * i + 1]));
+          a.z = fmaf(a.z, g, __uint_as_float(v[4 * i + 2]));
+          a.w = fmaf(a.w, g, __uint_as_float(v[4 * i + 3]));
+          if (save) sum[c * 8 + i] = a;
+          v[4 * i] = save ? 0u : __float_as_uint(a.x);
+          v[4 * i + 1] = save ? 0u : __float_as_uint(a.y);
+          v[4 * i + 2] = save ? 0u : __float_as_uint(a.z);
+          v[4 * i + 3] = save ? 0u : __float_as_uint(a.w);
+        }
+        tmem_st32(tO + c * 32, v);
+      }
+      tmem_wait_st();
+      if (save) p.part_ml[int64_t(slot) * 2] = m_used;
+    };
     bool more = take(cur);
     while (more) {
       const RowAt row = cur.row;
@@ -810,100 +851,109 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
       const float qk2 = cur.qk2;
       float m_used = -INFINITY, l_sum = 0.f;
       int seen = cur.seen, held = cur.held, seen_min = cur.seen_min;
-      for (int j = 0; j < nt; ++j) {
-        ok = __all_sync(0xffffffffu, wait(L::kS + x, s_phase));
-        if (!ok) break;
-        s_phase ^= 1;
-        tc_fence_after();
-        float sv[128];
-        {
-          uint32_t v[4][32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, v[c]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            reg_fence32(v[c]);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) sv[c * 32 + i] = __uint_as_float(v[c][i]);
-          }
-        }
-        if (seen_min < kTileKT) {
-#pragma unroll
-          for (int c = 0; c < 128; ++c) sv[c] = c < seen ? sv[c] : -INFINITY;
-        }
-        float m0 = sv[0], m1 = sv[1], m2 = sv[2], m3 = sv[3];
-#pragma unroll
-        for (int c = 4; c < 124; c += 8) {
-          m0 = fmax3(m0, sv[c + 0], sv[c + 1]);
-          m1 = fmax3(m1, sv[c + 2], sv[c + 3]);
-          m2 = fmax3(m2, sv[c + 4], sv[c + 5]);
-          m3 = fmax3(m3, sv[c + 6], sv[c + 7]);
-        }
-        m0 = fmax3(m0, sv[124], sv[125]);
-        m1 = fmax3(m1, sv[126], sv[127]);
-        const float m_tile = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * qk2;
-        float f = 1.f;
-        if (m_tile > m_used + (kRescale + kLift<DT>) || (m_used == -INFINITY && m_tile > -INFINITY)) {
-          f = ex2_approx(m_used - (m_tile - kLift<DT>));
-          m_used = m_tile - kLift<DT>;
-          l_sum *= f;
-        }
-        if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {   // O_X is stable: S_X(j) came after PV_X(j-1)
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t v[32];
-            tmem_ld32(tO + c * 32, v);
-            tmem_wait_ld();
-            reg_fence32(v);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-            tmem_st32(tO + c * 32, v);
-          }
-        }
-        const float shift = m_used == -INFINITY ? 0.f : -m_used;
-#pragma unroll
-        for (int c = 0; c < 128; c += 2) ffma2(sv[c], sv[c + 1], sv[c], sv[c + 1], qk2, qk2, shift, shift);
-#pragma unroll
-        for (int c = 0; c < 128; ++c) sv[c] = ex2_approx(sv[c]);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int c = 0; c < 32; ++c) pk[c] = pack2<DT>(sv[64 * q + 2 * c], sv[64 * q + 2 * c + 1]);
-          tmem_st32(tS + q * 32, pk);
-        }
-        // The values' rows behind the cache's end hold anything, and 0 * NaN
-        // must not reach O: tile A's threads clear them (PV_B comes after
-        // PV_A, which waits for these threads).
-        if (x == 0 && held < kTileKT) {
-          ok = __all_sync(0xffffffffu, wait(L::kFull + vr.slot, vr.phase));
+      int stop = min(nt, kSumTiles);
+      for (int j = 0; j < nt;) {
+        for (; j < stop; ++j) {
+          ok = __all_sync(0xffffffffu, wait(L::kS + x, s_phase));
           if (!ok) break;
-          if (r >= held) {
-            const uint32_t dst = sbase + L::kRing + vr.slot * L::kTile + r * 128;
+          s_phase ^= 1;
+          tc_fence_after();
+          float sv[128];
+          {
+            uint32_t v[4][32];
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c)
-              st_shared_v4(dst + (c >> 3) * L::kPanel + ((c & 7) << 4), make_uint4(0u, 0u, 0u, 0u));
+            for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, v[c]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              reg_fence32(v[c]);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) sv[c * 32 + i] = __uint_as_float(v[c][i]);
+            }
           }
-          fence_proxy_async_smem();
-        }
-        vr.skip(2);
-        seen -= kTileKT;
-        seen_min -= kTileKT;
-        held -= kTileKT;
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::kP + x));
-        float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f, a4 = 0.f, a5 = 0.f, a6 = 0.f, a7 = 0.f;
+          if (seen_min < kTileKT) {
 #pragma unroll
-        for (int c = 0; c < 128; c += 8) {
-          fadd2(a0, a1, a0, a1, sv[c + 0], sv[c + 1]);
-          fadd2(a2, a3, a2, a3, sv[c + 2], sv[c + 3]);
-          fadd2(a4, a5, a4, a5, sv[c + 4], sv[c + 5]);
-          fadd2(a6, a7, a6, a7, sv[c + 6], sv[c + 7]);
+            for (int c = 0; c < 128; ++c) sv[c] = c < seen ? sv[c] : -INFINITY;
+          }
+          float m0 = sv[0], m1 = sv[1], m2 = sv[2], m3 = sv[3];
+#pragma unroll
+          for (int c = 4; c < 124; c += 8) {
+            m0 = fmax3(m0, sv[c + 0], sv[c + 1]);
+            m1 = fmax3(m1, sv[c + 2], sv[c + 3]);
+            m2 = fmax3(m2, sv[c + 4], sv[c + 5]);
+            m3 = fmax3(m3, sv[c + 6], sv[c + 7]);
+          }
+          m0 = fmax3(m0, sv[124], sv[125]);
+          m1 = fmax3(m1, sv[126], sv[127]);
+          const float m_tile = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * qk2;
+          float f = 1.f;
+          if (m_tile > m_used + (kRescale + kLift<DT>) || (m_used == -INFINITY && m_tile > -INFINITY)) {
+            f = ex2_approx(m_used - (m_tile - kLift<DT>));
+            m_used = m_tile - kLift<DT>;
+            l_sum *= f;
+          }
+          if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {   // O_X is stable: S_X(j) came after PV_X(j-1)
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t v[32];
+              tmem_ld32(tO + c * 32, v);
+              tmem_wait_ld();
+              reg_fence32(v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+              tmem_st32(tO + c * 32, v);
+            }
+          }
+          const float shift = m_used == -INFINITY ? 0.f : -m_used;
+#pragma unroll
+          for (int c = 0; c < 128; c += 2) ffma2(sv[c], sv[c + 1], sv[c], sv[c + 1], qk2, qk2, shift, shift);
+#pragma unroll
+          for (int c = 0; c < 128; ++c) sv[c] = ex2_approx(sv[c]);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) pk[c] = pack2<DT>(sv[64 * q + 2 * c], sv[64 * q + 2 * c + 1]);
+            tmem_st32(tS + q * 32, pk);
+          }
+          // The values' rows behind the cache's end hold anything, and 0 * NaN
+          // must not reach O: tile A's threads clear them (PV_B comes after
+          // PV_A, which waits for these threads).
+          if (x == 0 && held < kTileKT) {
+            ok = __all_sync(0xffffffffu, wait(L::kFull + vr.slot, vr.phase));
+            if (!ok) break;
+            if (r >= held) {
+              const uint32_t dst = sbase + L::kRing + vr.slot * L::kTile + r * 128;
+#pragma unroll
+              for (int c = 0; c < D / 8; ++c)
+                st_shared_v4(dst + (c >> 3) * L::kPanel + ((c & 7) << 4), make_uint4(0u, 0u, 0u, 0u));
+            }
+            fence_proxy_async_smem();
+          }
+          vr.skip(2);
+          seen -= kTileKT;
+          seen_min -= kTileKT;
+          held -= kTileKT;
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::kP + x));
+          float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f, a4 = 0.f, a5 = 0.f, a6 = 0.f, a7 = 0.f;
+#pragma unroll
+          for (int c = 0; c < 128; c += 8) {
+            fadd2(a0, a1, a0, a1, sv[c + 0], sv[c + 1]);
+            fadd2(a2, a3, a2, a3, sv[c + 2], sv[c + 3]);
+            fadd2(a4, a5, a4, a5, sv[c + 4], sv[c + 5]);
+            fadd2(a6, a7, a6, a7, sv[c + 6], sv[c + 7]);
+          }
+          l_sum += ((a0 + a1) + (a2 + a3)) + ((a4 + a5) + (a6 + a7));
         }
-        l_sum += ((a0 + a1) + (a2 + a3)) + ((a4 + a5) + (a6 + a7));
+        if (!ok || j == nt) break;
+        ok = __all_sync(0xffffffffu, wait(L::kS + x, s_phase));      // O_X is stable then (above waits again)
+        if (!ok) break;
+        tc_fence_after();
+        move_sum(slot, m_used, j > kSumTiles, true);
+        stop = min(nt, j + kSumTiles);
       }
       if (!ok) break;
       more = take(cur);
@@ -913,6 +963,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         o_phase ^= 1;
         tc_fence_after();
       }
+      if (__builtin_expect(nt > kSumTiles, 0)) move_sum(slot, m_used, true, false);
       const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;      // no key: zeros
       auto load_o = [&](int c, uint32_t (&v)[32]) {            // 32 channels of this row
         if (nt > 0) {

@@ -8,7 +8,7 @@ import torch
 import kv_cache_compression_cas_b200 as vark
 from oracle import paged as ref
 from tests.helpers import check_status, status_word
-from tests.paged_cases import FP16_TINY, Pages, attention_bounds, norm_bound, rounded, values
+from tests.paged_cases import FP16_TINY, HALF, U32, Pages, attention_bounds, norm_bound, rounded, values
 from tests.test_gpu_paged import same_bits
 
 pytestmark = pytest.mark.gpu
@@ -53,15 +53,25 @@ def test_nan_and_infinity_in_a_normed_row(dtype, D, norm):
 
 
 # ------------------------------------------------------------------ attention
+def mma_sum_loss(keys, tiles):
+    """What sums on the tensor cores lose, of the mean of |v|: an MMA adds 16
+    products to an fp32 sum after cutting them off 2^-25 below its leading bit,
+    then cuts the sum to 24 bits: 16 * 2^-25 + 2^-23 = 20 * 2^-25 for 16 keys.  A
+    sum takes at most 256 * 128 keys on tcgen05, an eighth of the keys (a warp's)
+    in the kernels of few rows."""
+    return (min(keys, 256 * 128) if tiles else keys / 8) * 1.25 * 2.0 ** -25
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("gap", [17.0, 18.0, 10.0])
 @pytest.mark.parametrize("n,G", [(1, 1), (1, 20), (40, 4)])
-@pytest.mark.parametrize("value", [0.0])
+@pytest.mark.parametrize("value", [0.0, None])
 def test_one_key_outweighs_a_long_cache(dtype, D, gap, n, G, value):
     """The first of 65536 keys has a logit `gap` above the others, which are
     alike and whose weights together are felt all the same; its value is 0, so
-    the others make all of the output.  160 sequences over the same pages, so
+    the others make all of the output, or as theirs, so that each adds next to
+    nothing to a large sum.  160 sequences over the same pages, so
     that a CTA has long runs of keys (one is half a cache and more); every
     kernel: 16, 32 and 256 rows."""
     rng = np.random.default_rng(int(gap) * 1000 + D + G)
@@ -70,7 +80,8 @@ def test_one_key_outweighs_a_long_cache(dtype, D, gap, n, G, value):
     k[0, 0, 0] = np.float16(gap / np.sqrt(D))           # with q = 1: D of them / sqrt(D)
     k = rounded(k, dtype)
     v = rounded(rng.uniform(0.5, 1.5, (keys // ps, 1, ps, D)), dtype)
-    v[0, 0, 0] = value
+    if value is not None:
+        v[0, 0, 0] = value
     table = np.arange(keys // ps, dtype=np.int32)[None]
     lens, cu = np.array([keys], dtype=np.int32), np.array([0, 1], dtype=np.int32)
     one = np.ones((1, 1, D))
@@ -91,5 +102,36 @@ def test_one_key_outweighs_a_long_cache(dtype, D, gap, n, G, value):
         # the bound allows every probability FP16_TINY of the largest, times 6 for |v|; the
         # reference 2^7 below the maximum makes it 2^-7 of that, and |v| is at most 1.5
         b_out += keys * FP16_TINY * (1.5 * 2.0 ** -7 - 6.0)
+    b_out += mma_sum_loss(keys, n > 1) * mean_abs
     assert (np.abs(values(out) - o[0, 0]) <= b_out[0, 0]).all()
     assert (np.abs(values(lse) - z[0, 0]) <= b_lse[0, 0]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,G", [(1, 1), (1, 20), (40, 4)])
+def test_mean_of_a_million_keys(dtype, D, n, G):
+    """Logits all 0 (a temperature of 0): the output is the mean of the values,
+    the log-sum the logarithm of their number.  160 sequences over the same
+    eight pages, again and again."""
+    rng = np.random.default_rng(D + G)
+    B, keys, ps = 160, 1 << 20, 256
+    v = rounded(rng.uniform(0.5, 1.5, (8, 1, ps, D)), dtype)
+    k = rounded(rng.standard_normal((8, 1, ps, D)), dtype)
+    want = values(v).reshape(-1, D).mean(0)
+    N = B * n
+    out = torch.empty(N, G, D, dtype=v.dtype, device="cuda")
+    lse = torch.empty(N, G, device="cuda")
+    ws = torch.empty(vark.vark_paged_attention_workspace(N, B, G, 1, D, ps, keys // ps), dtype=torch.uint8,
+                     device="cuda")
+    st = status_word()
+    vark.vark_paged_attention(torch.ones(N, G, D, dtype=v.dtype, device="cuda"),
+                              torch.arange(B + 1, dtype=torch.int32, device="cuda") * n, k.cuda(), v.cuda(),
+                              torch.arange(keys // ps, dtype=torch.int32, device="cuda").remainder(8).expand(B, -1)
+                              .contiguous(), torch.full((B,), keys, dtype=torch.int32, device="cuda"),
+                              torch.zeros(G, device="cuda"), False, out, lse, ws, st)
+    check_status(st)
+    # every probability is a power of two and their sum exact; each of 80 partial sums rounds once
+    bound = want * (HALF[dtype] + mma_sum_loss(keys, n > 1) + 80 * U32)
+    assert (np.abs(values(out) - want) <= bound).all()
+    assert (np.abs(values(lse) - np.log(keys)) <= 16 * U32 * np.log(keys)).all()

@@ -612,6 +612,9 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
   auto wait = [&](int i, int phase) {
     return mbar_wait(bar(i), uint32_t(phase), abort_flag, p.status, p.wait_limit_ns);
   };
+  // One answer for a warp: a wait that one lane sees completed and another given
+  // up must not part them.
+  auto wait_all = [&](int i, int phase) { return __all_sync(0xffffffffu, wait(i, phase)) != 0; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -705,6 +708,9 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
               commit(lead, bar(L::kO + x));
             }
           }
+          // (asked once a key tile, behind the MMAs: a lane that gave up above
+          // left nothing that the others wait for in lockstep)
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (j > 0) {
             commit(lead, bar(L::kEmpty + vr.slot));
@@ -735,7 +741,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
       bool ok = true;
       while (ok && next_segment(p, sg)) {
         if (seen_tiles(p, sg) == 0 || (x == 1 && sg.x.n * p.G - sg.tile * kTileR <= 128)) continue;
-        if (uses > 0) ok = __all_sync(0xffffffffu, wait(L::kQFree + x, (uses - 1) & 1));
+        if (uses > 0) ok = wait_all(L::kQFree + x, (uses - 1) & 1);
         if (!ok) break;
         ++uses;
         bool turned = false;
@@ -854,7 +860,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
       int stop = min(nt, kSumTiles);
       for (int j = 0; j < nt;) {
         for (; j < stop; ++j) {
-          ok = __all_sync(0xffffffffu, wait(L::kS + x, s_phase));
+          ok = wait_all(L::kS + x, s_phase);
           if (!ok) break;
           s_phase ^= 1;
           tc_fence_after();
@@ -920,7 +926,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
           // must not reach O: tile A's threads clear them (PV_B comes after
           // PV_A, which waits for these threads).
           if (x == 0 && held < kTileKT) {
-            ok = __all_sync(0xffffffffu, wait(L::kFull + vr.slot, vr.phase));
+            ok = wait_all(L::kFull + vr.slot, vr.phase);
             if (!ok) break;
             if (r >= held) {
               const uint32_t dst = sbase + L::kRing + vr.slot * L::kTile + r * 128;
@@ -949,7 +955,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
           l_sum += ((a0 + a1) + (a2 + a3)) + ((a4 + a5) + (a6 + a7));
         }
         if (!ok || j == nt) break;
-        ok = __all_sync(0xffffffffu, wait(L::kS + x, s_phase));      // O_X is stable then (above waits again)
+        ok = wait_all(L::kS + x, s_phase);      // O_X is stable then (above waits again)
         if (!ok) break;
         tc_fence_after();
         move_sum(slot, m_used, j > kSumTiles, true);
@@ -958,7 +964,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
       if (!ok) break;
       more = take(cur);
       if (nt > 0) {
-        ok = __all_sync(0xffffffffu, wait(L::kO + x, o_phase));
+        ok = wait_all(L::kO + x, o_phase);
         if (!ok) break;
         o_phase ^= 1;
         tc_fence_after();

@@ -730,7 +730,8 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
       // -------------------------------------------------------- queries
       // Tile x's 128 rows, 128-byte swizzled, D / 8 lanes a row.  Under a
       // negative temperature the query's sign is turned instead, so the
-      // largest score gives the largest logit; under 0 the query is 0.
+      // largest score gives the largest logit; under 0, and where the factor of
+      // the scores rounds to 0, the query is 0.
       constexpr int kRowLanes = D / 8, kRowsAt = 32 / kRowLanes;
       const int x = warp - 2;
       const uint32_t sq = sbase + L::kQ + x * L::kTile;
@@ -749,7 +750,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         for (int q = 0; q < 4; ++q) {
           const RowAt row = row_at(p, sg, x * 128 + q * 32 + lane);
           const float tau = p.tau != nullptr && row.token >= 0 ? p.tau[row.head] : 1.f;
-          const int64_t off = row.token < 0 || tau == 0.f ? -1 : row.token * p.qs[0] + row.head * p.qs[1];
+          const int64_t off = row.token < 0 || p.scale_log2 * tau == 0.f ? -1 : row.token * p.qs[0] + row.head * p.qs[1];
           turned |= tau < 0.f;
 #pragma unroll 4
           for (int it = 0; it < 32 / kRowsAt; ++it) {
@@ -806,8 +807,8 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
       w.row = row_at(p, sg, x * 128 + r);
       w.qk2 = p.scale_log2;
       if (p.tau != nullptr && w.row.token >= 0) {
-        const float tau = p.tau[w.row.head];
-        w.qk2 = tau == 0.f ? 1.f : w.qk2 * fabsf(tau);
+        const float f = w.qk2 * fabsf(p.tau[w.row.head]);
+        w.qk2 = f == 0.f ? 1.f : f;
       }
       w.nt = seen_tiles(p, sg);
       // (a row that does not exist needs no mask: nothing reads what it makes)

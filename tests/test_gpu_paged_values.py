@@ -1,6 +1,6 @@
 """The serving calls at values and sizes where a kernel can lose what the
 definition keeps: NaN and infinities in a norm's rows; caches where one key
-outweighs the others."""
+outweighs the others; temperatures next to 0."""
 import numpy as np
 import pytest
 import torch
@@ -9,7 +9,7 @@ import kv_cache_compression_cas_b200 as vark
 from oracle import paged as ref
 from tests.helpers import check_status, status_word
 from tests.paged_cases import FP16_TINY, HALF, U32, Pages, attention_bounds, norm_bound, rounded, values
-from tests.test_gpu_paged import same_bits
+from tests.test_gpu_paged import compare, run_attention, same_bits
 
 pytestmark = pytest.mark.gpu
 
@@ -135,3 +135,17 @@ def test_mean_of_a_million_keys(dtype, D, n, G):
     bound = want * (HALF[dtype] + mma_sum_loss(keys, n > 1) + 80 * U32)
     assert (np.abs(values(out) - want) <= bound).all()
     assert (np.abs(values(lse) - np.log(keys)) <= 16 * U32 * np.log(keys)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 3, 90])
+def test_temperatures_next_to_zero(dtype, D, n):
+    """The smallest temperatures of either sign, some of whose products with
+    log2(e) / sqrt(D) are 0 in fp32: masked keys stay masked in every kernel."""
+    rng = np.random.default_rng(D + n)
+    pg = Pages(rng, dtype, [n, n], [n + 40, n + 300], 1, D, 32, False)
+    tau = np.array([1e-45, -1e-45, 3e-45, -4e-45, 1e-44, 1e-38, -1e-30, 0.0], dtype=np.float32)
+    q = rounded(rng.standard_normal((2 * n, len(tau), D)), dtype)
+    out, lse = run_attention(pg, q, tau, True)
+    compare(pg, q, tau, True, out, lse, dtype)

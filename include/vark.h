@@ -594,9 +594,9 @@ enum vark_norm {
  *                read, and the [B][H][T][D] of the dense attention calls
  *                written, in place.  Either may be NULL (with its strides,
  *                output and weight).
- *   q_out, k_out dev, by their own strides (at least D: no two rows at one
- *                place); may be q, k themselves (same strides), else they must
- *                not overlap the inputs.
+ *   q_out, k_out dev, by their own strides (no two rows of one may share an
+ *                element: VARK_E_ALIGN); may be q, k themselves (same strides),
+ *                else they must not overlap the inputs or each other.
  *   B, T         >= 0, B * T < 2^31 - 128;  Hq, Hk >= 1, <= 65536;  D 64 or 128.
  *   norm         vark_norm;  eps >= 0 (L2: 0 or a normal number).  A row of
  *                zeros with eps = 0 has no norm and gives NaN; a NaN in a row
@@ -657,8 +657,9 @@ int64_t vark_paged_attention_workspace(int64_t n_tokens, int B, int Hq, int Hkv,
  * Logit tau[h] * (q . k) / sqrt(D); softmax over the rows seen.  A query that
  * sees no row gets a zero output and -inf in lse.
  *   q, out       dev 16-bit; the row of (token, head) starts at token *
- *                strides[0] + head * strides[1] (as vark_paged_append; those of
- *                out at least D); out must not overlap q.
+ *                strides[0] + head * strides[1] (as vark_paged_append); those of
+ *                out are at least D, and it is the caller's to see that no two
+ *                of its rows share an element, nor any with q.
  *   tau          dev fp32 [Hq] or NULL (ones).
  *   lse          dev fp32 [n_tokens][Hq] out, or NULL: log of the sum of exp of
  *                the logits, with which outputs over disjoint caches combine.

@@ -385,7 +385,7 @@ extern "C" int vark_qk_norm_rope(int dtype, const uint16_t* q, const int64_t* q_
     const int64_t n[3] = {B, T, Hq};
     p.t[0] = RowTensor{q, q_out, q_weight, {0, 0, 0}, {0, 0, 0}, Hq};
     if (!take_strides(p.t[0].ss, q_strides, n, 3, 0) || !take_strides(p.t[0].ds, q_out_strides, n, 3, D) ||
-        !aligned16(q) || !aligned16(q_out))
+        !rows_apart(p.t[0].ds, n, 3, D) || !aligned16(q) || !aligned16(q_out))
       return VARK_E_ALIGN;
     if (!in_place_alike(p.t[0])) return VARK_E_ARG;
   }
@@ -393,7 +393,7 @@ extern "C" int vark_qk_norm_rope(int dtype, const uint16_t* q, const int64_t* q_
     const int64_t n[3] = {B, T, Hk};
     p.t[1] = RowTensor{k, k_out, k_weight, {0, 0, 0}, {0, 0, 0}, Hk};
     if (!take_strides(p.t[1].ss, k_strides, n, 3, 0) || !take_strides(p.t[1].ds, k_out_strides, n, 3, D) ||
-        !aligned16(k) || !aligned16(k_out))
+        !rows_apart(p.t[1].ds, n, 3, D) || !aligned16(k) || !aligned16(k_out))
       return VARK_E_ALIGN;
     if (!in_place_alike(p.t[1])) return VARK_E_ARG;
   }

@@ -82,12 +82,30 @@ struct Pages {
 };
 
 // Strides of rows of 16-byte vectors (host): multiples of 8 elements, at least
-// `least` (0 for rows that are read, D for rows that are written: no two at one
-// address); the stride of an axis of one entry is not looked at.
+// `least` (0 for rows that are read, D for rows that are written); the stride of
+// an axis of one entry is not looked at.
 inline bool take_strides(int64_t* to, const int64_t* s, const int64_t* extent, int n, int least) {
   for (int i = 0; i < n; ++i) {
     to[i] = extent[i] > 1 ? s[i] : 0;
     if (extent[i] > 1 && (s[i] < least || s[i] % 8 != 0)) return false;
+  }
+  return true;
+}
+
+// No two written rows share an element (host, strides as taken above): from the
+// smallest stride on, every axis steps over all that the ones before it span.
+inline bool rows_apart(const int64_t* s, const int64_t* extent, int n, int D) {
+  int64_t span = D, below = 0;
+  for (int k = 0; k < n; ++k) {           // the k-th smallest stride, of few
+    int at = -1;
+    for (int i = 0; i < n; ++i)
+      if (extent[i] > 1 && s[i] > below && (at < 0 || s[i] < s[at])) at = i;
+    if (at < 0) break;
+    int alike = 0;                        // two axes of one stride lie on each other
+    for (int i = 0; i < n; ++i) alike += extent[i] > 1 && s[i] == s[at];
+    if (alike > 1 || s[at] < span) return false;
+    below = s[at];
+    span = s[at] > (INT64_MAX - span) / extent[at] ? INT64_MAX : span + s[at] * (extent[at] - 1);
   }
   return true;
 }

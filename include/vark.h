@@ -641,8 +641,9 @@ int vark_paged_append(int dtype, const uint16_t* k, const int64_t* k_strides, co
                       const int32_t* positions, int32_t* dev_status, void* stream);
 
 /*
- * vark_paged_attention_workspace -- host.  Bytes of workspace that
- * vark_paged_attention wants for these shapes (> 0), or a negative status.
+ * vark_paged_attention_workspace -- host.  Bytes of workspace (> 0) that serve
+ * vark_paged_attention at these shapes and at any fewer tokens and sequences
+ * (at most 40 MB), or a negative status.
  */
 int64_t vark_paged_attention_workspace(int64_t n_tokens, int B, int Hq, int Hkv, int D, int page_size,
                                        int max_pages);

@@ -850,7 +850,8 @@ def vark_paged_append(k, v, cu_tokens, k_pages, v_pages, page_table, cache_len, 
 
 def vark_paged_attention_workspace(n_tokens: int, batch: int, q_heads: int, kv_heads: int, D: int, page_size: int,
                                    max_pages: int) -> int:
-    """Host: bytes of workspace for vark_paged_attention at these shapes."""
+    """Host: bytes of workspace for vark_paged_attention at these shapes, and at
+    any fewer tokens and sequences."""
     n = int(_load().vark_paged_attention_workspace(int(n_tokens), int(batch), int(q_heads), int(kv_heads), int(D),
                                                    int(page_size), int(max_pages)))
     if n < 0:

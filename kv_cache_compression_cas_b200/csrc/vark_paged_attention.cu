@@ -1669,7 +1669,7 @@ extern "C" int64_t vark_paged_attention_workspace(int64_t n_tokens, int B, int H
                                                   int max_pages) {
   if (const int rc = check_shapes(n_tokens, B, Hq, Hkv, D)) return rc;
   if (page_size < 1 || max_pages < 1) return VARK_E_SHAPE;
-  return workspace_bytes_for(choose_rows(n_tokens, B, Hq, Hkv, D), D);
+  return workspace_bytes_for(choose_rows(n_tokens, 1, Hq, Hkv, D), D);      // (fewer sequences: as many rows or more)
 }
 
 extern "C" int vark_paged_attention(int dtype, const uint16_t* q, const int64_t* q_strides, int64_t n_tokens, int B,
@@ -1688,8 +1688,8 @@ extern "C" int vark_paged_attention(int dtype, const uint16_t* q, const int64_t*
   if (!q || !q_strides || !cu_tokens || !k_pages || !v_pages || !page_table || !cache_len || !out || !out_strides ||
       !workspace)
     return VARK_E_ARG;
-  if (workspace_bytes < vark_paged_attention_workspace(n_tokens, B, Hq, Hkv, D, page_size, max_pages))
-    return VARK_E_ARG;
+  const int rows = choose_rows(n_tokens, B, Hq, Hkv, D);
+  if (workspace_bytes < workspace_bytes_for(rows, D)) return VARK_E_ARG;
   const int64_t extent[2] = {n_tokens, Hq};
   if (!take_strides(p.qs, q_strides, extent, 2, 0) || !take_strides(p.os, out_strides, extent, 2, D))
     return VARK_E_ALIGN;
@@ -1704,7 +1704,6 @@ extern "C" int vark_paged_attention(int dtype, const uint16_t* q, const int64_t*
   p.by_group = FastDiv::of(p.G);
   p.by_heads = FastDiv::of(Hkv);
   p.scale_log2 = kLog2e / sqrtf(float(D));
-  const int rows = choose_rows(n_tokens, B, Hq, Hkv, D);
   p.tokens_per_tile = rows / p.G;
   p.tile_step = rows * kUnit / p.G;
   p.part_ml = static_cast<float*>(workspace);

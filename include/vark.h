@@ -673,7 +673,9 @@ int64_t vark_paged_attention_workspace(int64_t n_tokens, int B, int Hq, int Hkv,
  * The tensor cores cut a product off 2^-25 below the sum they add it to: an
  *   output may lose 1.25 2^-25 of the mean |v| for each of up to 32768 keys (few
  *   rows a kv head: of an eighth of the keys).
- * Limits: n_tokens * Hq < 2^30, B * Hkv <= 2^24.
+ * Limits: n_tokens * Hq < 2^30, B * Hkv <= 2^24, max_pages * page_size <
+ *   2^31 - 1024, and B / 2 * n_tokens * Hq * (max_pages * page_size + n_tokens)
+ *   < 4.5e18 (one sequence of any size is within it).
  * Errors: VARK_E_ARG, VARK_E_SHAPE, VARK_E_ALIGN, VARK_E_CUDA, VARK_E_DEVICE;
  *   *dev_status as vark_scas_accumulate, and the tables' VARK_E_SHAPE.
  */

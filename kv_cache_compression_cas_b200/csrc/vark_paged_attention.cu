@@ -1657,6 +1657,15 @@ static int check_shapes(int64_t n_tokens, int B, int Hq, int Hkv, int D) {
   return VARK_OK;
 }
 
+// The plan's units (see Entry) add up in 64 bits whatever the tables hold:
+// offsets that go up and down give at most every other sequence all tokens
+// (recorded, but by then they are summed).
+static bool plan_fits(int64_t n_tokens, int B, int Hq, int Hkv, int64_t max_rows) {
+  const double row_tiles = double((int64_t(B) + 1) / 2) * (double(n_tokens) * Hq / 16 + Hkv);
+  const double heaviest = kUnit * (double(max_rows) + double(n_tokens) + 512);
+  return row_tiles * heaviest < 4.6e18;
+}
+
 static int64_t workspace_bytes_for(int rows, int D) { return int64_t(kCtas) * 2 * rows * (D + 2) * 4; }
 
 }  // namespace paged
@@ -1684,6 +1693,7 @@ extern "C" int vark_paged_attention(int dtype, const uint16_t* q, const int64_t*
   if (rc) return rc;
   AttnParams p;
   if ((rc = make_pages(&p.pg, page_table, cache_len, n_pages, page_size, max_pages, Hkv, head_pages))) return rc;
+  if (!plan_fits(n_tokens, B, Hq, Hkv, int64_t(max_pages) * page_size)) return VARK_E_SHAPE;
   if (n_tokens == 0 || B == 0) return check_device_sm100();       // empty tensors have no addresses to look at
   if (!q || !q_strides || !cu_tokens || !k_pages || !v_pages || !page_table || !cache_len || !out || !out_strides ||
       !workspace)

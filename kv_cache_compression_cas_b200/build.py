@@ -69,11 +69,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
-def build_call(force: bool = False, verbose: bool = False) -> str:
+def build_call(force: bool = False, verbose: bool = False) -> str | None:
+    """The marshalling module, or None where there is no torch to build it
+    against: the library is for C programs too."""
     newest = max(os.path.getmtime(f) for f in (CALL_SRC, os.path.join(INCLUDE, "vark.h")))
     if not force and os.path.exists(CALL) and os.path.getmtime(CALL) >= newest:
         return CALL
     spec = importlib.util.find_spec("torch")       # located, not imported
+    if spec is None:
+        return None
     torch_dir = os.path.dirname(spec.origin)
     inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
     cuda = os.path.dirname(os.path.dirname(NVCC))
@@ -94,4 +98,5 @@ def build_call(force: bool = False, verbose: bool = False) -> str:
 if __name__ == "__main__":
     build(force="--force" in sys.argv, verbose="--verbose" in sys.argv)
     print(LIB)
-    print(build_call(force="--force" in sys.argv, verbose="--verbose" in sys.argv))
+    print(build_call(force="--force" in sys.argv, verbose="--verbose" in sys.argv)
+          or f"no torch: {os.path.basename(CALL)} is not built")

@@ -18,12 +18,11 @@
 #include <cstdlib>
 
 #include "vark_paged.cuh"
+#include "vark_paged_plan.cuh"
 
 namespace vark {
 namespace paged {
 
-constexpr int kCtas = 148;             // one persistent CTA per SM
-constexpr int kTileR = 256;            // rows of an item of the tiles kernel
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;       // log2: a running maximum may lag by this much
@@ -36,22 +35,6 @@ constexpr float kRescale = 8.0f;       // log2: a running maximum may lag by thi
 // 44% too heavy and 18 below were lost.
 template <int DT>
 constexpr float kLift = DT == VARK_FP16 ? 7.0f : 0.0f;
-
-// Division by a number the host knows, by a product (a division costs 130
-// cycles of latency, and several lie on the way to a CTA's first load).  Of
-// the divisor d, with s = ceil(log2 d): mul = floor(2^32 (2^s - d) / d) + 1;
-// x / d = (hi32(x mul) + x) >> s for 0 <= x < 2^31.
-struct FastDiv {
-  uint32_t mul, shift;
-  static FastDiv of(int d) {
-    FastDiv f;
-    f.shift = 0;
-    while ((uint32_t(1) << f.shift) < uint32_t(d)) ++f.shift;
-    f.mul = uint32_t(((uint64_t(1) << 32) * ((uint64_t(1) << f.shift) - uint32_t(d))) / uint32_t(d) + 1);
-    return f;
-  }
-  VARK_DEV int operator()(int x) const { return int((__umulhi(uint32_t(x), mul) + uint32_t(x)) >> shift); }
-};
 
 struct AttnParams {
   const uint16_t* q;
@@ -72,116 +55,30 @@ struct AttnParams {
   int32_t* status;
   uint64_t wait_limit_ns;
   int withhold;            // test hook: key tiles a CTA loads before it stops (-1: all)
+
+  // Row e of the length table.  Lengths and token offsets that do not fit the
+  // arguments leave it without work and are recorded.
+  template <int R, int KT>
+  VARK_DEV Entry entry(int e) const {
+    Entry x;
+    const int b = pg.table_heads > 1 ? by_heads(e) : e;
+    x.first = __ldcg(cu + b);     // (past L1: the join plans before it waits for the kernels ahead of it)
+    const int end = __ldcg(cu + b + 1);
+    x.len = __ldcg(pg.len + e);
+    if (x.first < 0 || end < x.first || end > N || x.len < 0 || (x.len - 1) >> pg.log2_page >= pg.max_pages) {
+      record(status, VARK_E_SHAPE);
+      x.first = x.n = x.len = 0;
+    } else {
+      x.n = end - x.first;
+    }
+    x.weigh<R, KT>(*this);
+    return x;
+  }
 };
 
 // ------------------------------------------------------------------ the plan
-// An entry is one row of the length table: a sequence (shared pages, all kv
-// heads) or a (sequence, head).  Its items, head after head and row tile after
-// row tile, weigh what they cost, in sixteenths of a key: kItemCost tiles for
-// starting and finishing one, and the keys its rows see -- which under a causal
-// mask grow by the tokens of a tile from one row tile to the next, so the
-// weights and their sums have a closed form.  (Equal weights left causal
-// prompts with shares of 0.6 to 1.5 times the mean work.)
-constexpr int kUnit = 16;
-// Key tiles that an item counts for besides its own.  Of 0 / 1 / 2 / 3 / 5: 64
-// sequences decoding 202 / 190 / 190 / 192 / 196 us, drafted tokens of 64
-// channels 69 / 51 / 47 / 47 / 49, prompts 645 / 516 / 458 / 455 / 483.
-constexpr int kItemCost = 2;
-// Where there is a CTA for every item of 256 rows, cutting one up must save more
-// than this many key tiles' time, which its partial results and the join cost:
-// 200 tokens over 16 rows (32 heads of 128) 25.2 -> 19.4 us whole, 8 times 100
-// over 1000 46.5 -> 35.9; at 9 one chunk of 64 over 700 loses 22.8 -> 25.1.
-constexpr int kCutTiles = 6;
-// a / b of non-negative numbers, in 32 bits where they allow it (64 take ten
-// times as long).
-VARK_DEV int64_t quotient(int64_t a, int64_t b) {
-  return ((a | b) >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
-}
-struct Entry {
-  int first, n;            // first token, tokens
-  int len;                 // cache rows
-  int row_tiles, heads;    // row tiles of a head, kv heads of the entry
-  int slope;               // weight of row tile t: weight0 + t * slope
-  int64_t weight0;
+// The arithmetic is in vark_paged_plan.cuh; here the scan over the tables.
 
-  VARK_DEV int64_t sum(int t) const { return t * weight0 + int64_t(slope) * t * (t - 1) / 2; }   // of tiles 0 .. t-1
-  VARK_DEV int64_t head_units() const { return sum(row_tiles); }
-  VARK_DEV int64_t units() const { return heads * head_units(); }
-  VARK_DEV int64_t longest() const { return row_tiles == 0 ? 0 : weight0 + int64_t(row_tiles - 1) * slope; }
-  VARK_DEV void count_items() {                // every item weighs one unit
-    slope = 0;
-    weight0 = 1;
-  }
-  // The row tile that holds unit `off` of a head.
-  VARK_DEV int tile_of(int64_t off) const {
-    int t;
-    if (row_tiles == 1) return 0;
-    if (slope == 0) {
-      t = int(quotient(off, weight0));
-    } else {
-      const double lin = double(weight0) - 0.5 * slope;
-      t = int((sqrt(lin * lin + 2.0 * slope * double(off)) - lin) / slope);
-    }
-    t = max(0, min(row_tiles - 1, t));
-    while (t > 0 && sum(t) > off) --t;
-    while (t + 1 < row_tiles && sum(t + 1) <= off) ++t;
-    return t;
-  }
-};
-
-// Lengths and token offsets that do not fit the arguments leave the entry
-// without work and are recorded.
-template <int R, int KT>
-VARK_DEV Entry load_entry(const AttnParams& p, int e) {
-  Entry x;
-  const int b = p.pg.table_heads > 1 ? p.by_heads(e) : e;
-  x.first = __ldcg(p.cu + b);     // (past L1: the join plans before it waits for the kernels ahead of it)
-  const int end = __ldcg(p.cu + b + 1);
-  x.len = __ldcg(p.pg.len + e);
-  if (x.first < 0 || end < x.first || end > p.N || x.len < 0 || (x.len - 1) >> p.pg.log2_page >= p.pg.max_pages) {
-    record(p.status, VARK_E_SHAPE);
-    x.first = x.n = x.len = 0;
-  } else {
-    x.n = end - x.first;
-  }
-  x.row_tiles = (x.n * p.G + R - 1) / R;
-  x.heads = p.pg.table_heads > 1 ? 1 : p.pg.heads;
-  x.slope = p.causal && x.row_tiles > 1 ? p.tile_step : 0;
-  const int seen0 = x.slope ? min(x.len, max(0, x.len - x.n) + p.tokens_per_tile) : x.len;     // by the first row tile
-  x.weight0 = int64_t(kUnit) * (int64_t(kItemCost) * KT + seen0);
-  return x;
-}
-
-// Where an item's key tiles lie in its units [from, to): after its fixed cost;
-// the tile that unit u has come to (the last unit is the end of all tiles).
-struct ItemPlace {
-  int64_t from, to;
-  int key_tiles;
-  template <int KT>
-  VARK_DEV int tile_at(const AttnParams& p, int64_t u) const {
-    if (u >= to) return key_tiles;
-    const int64_t k = (u - from) / (kUnit * KT) - kItemCost;
-    return int(max(int64_t(0), min(int64_t(key_tiles), k)));
-  }
-};
-
-struct Share {
-  int ctas;                // shares of the call: extra of them have per + 1 units, the others per
-  int64_t per, extra;
-  int64_t u0, u1;          // this CTA's units
-  struct Place {
-    int e;                 // an entry, its first unit, and itself
-    int64_t base;
-    Entry x;
-  };
-  Place first, last;       // where units u0 and u1 - 1 lie (last: on request)
-
-  VARK_DEV int64_t begin(int c) const { return per * c + min(int64_t(c), extra); }
-  VARK_DEV int holder(int64_t u) const {       // the share that unit u is in
-    const int64_t wide = extra * (per + 1);
-    return u < wide ? int(quotient(u, per + 1)) : int(extra + quotient(u - wide, per));
-  }
-};
 
 // Running sum over the lanes of a warp.
 template <typename T>
@@ -220,7 +117,7 @@ VARK_DEV Share find_share(const AttnParams& p, int cta) {
   int64_t sum = 0, items = 0, longest = 0;
   Entry x = {};
   for (int e = e0; e < e1; ++e) {
-    x = load_entry<R, KT>(p, e);
+    x = p.entry<R, KT>(e);
     sum += x.units();
     if (kMayCount) {
       items += int64_t(x.heads) * x.row_tiles;
@@ -241,7 +138,7 @@ VARK_DEV Share find_share(const AttnParams& p, int cta) {
   bool one_each = false;             // every item weighs one unit: none is cut
   if (kMayCount) {
     const int tiles = __reduce_max_sync(0xffffffffu, lane < kWarps ? warp_longest[lane] : 0);
-    if ((tiles - kCutTiles) * (kTile * kCtas) <= total) {        // (the same for every thread)
+    if (worth_whole<KT>(tiles, total)) {        // (the same for every thread)
       const int own = int(min(items, int64_t(kCtas + 1)));
       const int incl_items = lane_sums(own, lane);
       if (lane == 31) warp_items[warp] = incl_items;
@@ -258,13 +155,7 @@ VARK_DEV Share find_share(const AttnParams& p, int cta) {
       }
     }
   }
-  s.ctas = int(min(int64_t(kCtas), total));
-  s.per = 1;
-  s.extra = 0;
-  if (total > kCtas) {
-    s.per = quotient(total, kCtas);
-    s.extra = total - s.per * kCtas;
-  }
+  s.split(total);
   s.u0 = s.u1 = 0;
   if (cta >= s.ctas) return s;   // the same for every thread
   s.u0 = s.begin(cta);
@@ -277,7 +168,7 @@ VARK_DEV Share find_share(const AttnParams& p, int cta) {
     int64_t base = from;
     for (int e = e0; e < e1; ++e) {
       if (chunk > 1) {                                // (else it is the one just read)
-        x = load_entry<R, KT>(p, e);
+        x = p.entry<R, KT>(e);
         if (one_each) x.count_items();
       }
       const int64_t w = x.units();
@@ -293,71 +184,6 @@ VARK_DEV Share find_share(const AttnParams& p, int cta) {
   if (LAST) s.last = found[1];
   return s;
 }
-
-// The runs of key tiles [k0, k1) of a share, item after item.
-template <int R, int KT>
-struct Segments {
-  Entry x;
-  int e, i;                // entry, head within it
-  int64_t u, u1;           // next unit, end of the share
-  ItemPlace at;            // the item of the segment
-  int tile, h, k0, k1;
-
-  VARK_DEV void start(const AttnParams& p, const Share& s) {
-    e = s.first.e;
-    x = s.first.x;
-    u = s.u0;
-    u1 = s.u1;
-    find(p, s.first.base, u);
-  }
-  VARK_DEV bool next(const AttnParams& p) {
-    while (u < u1) {
-      if (u == at.to) step(p);
-      const int64_t stop = min(at.to, u1);
-      k0 = at.tile_at<KT>(p, u);
-      k1 = at.tile_at<KT>(p, stop);
-      u = stop;
-      if (k0 < k1) return true;      // (else a share's end fell into the item's fixed cost)
-    }
-    return false;
-  }
-  VARK_DEV bool whole() const { return k0 == 0 && k1 == at.key_tiles; }
-  // The item of entry e, whose first unit is `base`, that holds unit v.
-  VARK_DEV void find(const AttnParams& p, int64_t base, int64_t v) {
-    const int64_t per_head = x.head_units();
-    int64_t off = v - base;
-    i = x.heads == 1 ? 0 : int(quotient(off, per_head));
-    off -= i * per_head;
-    tile = x.tile_of(off);
-    at.from = base + i * per_head + x.sum(tile);
-    place(p);
-  }
-  VARK_DEV void step(const AttnParams& p) {
-    at.from = at.to;
-    if (++tile == x.row_tiles) {
-      tile = 0;
-      if (++i == x.heads) {
-        i = 0;
-        const bool items = R == kTileR && x.weight0 == 1;      // (see count_items)
-        do x = load_entry<R, KT>(p, ++e);
-        while (x.row_tiles == 0);
-        if (items) x.count_items();
-      }
-    }
-    place(p);
-  }
-  VARK_DEV void place(const AttnParams& p) {
-    h = p.pg.table_heads > 1 ? e - p.by_heads(e) * p.pg.heads : i;
-    at.to = at.from + x.weight0 + int64_t(tile) * x.slope;
-    at.key_tiles = max(1, (limit(p) + KT - 1) / KT);
-  }
-  // Keys that some row of the tile sees.
-  VARK_DEV int limit(const AttnParams& p) const {
-    if (!p.causal) return x.len;
-    const int last = min(x.n - 1, p.by_group(tile * R + R - 1));
-    return max(0, x.len - x.n + last + 1);
-  }
-};
 
 struct RowAt {
   int token, head;         // token of the batch, query head; token < 0: no such row
@@ -425,7 +251,6 @@ VARK_DEV void store_row8(const AttnParams& p, const RowAt& a, int d0, const floa
 // tiles; every 128 tiles 2.5% of the chunk above.
 constexpr int kSumTiles = 256;
 constexpr int kTileThreads = 384;
-constexpr int kTileKT = 128;
 constexpr int kMaxSmem = 232448;
 
 VARK_DEV uint32_t elect_one() {
@@ -816,7 +641,7 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
       w.held = sg.x.len - sg.k0 * kTileKT;
       w.seen_min = __reduce_min_sync(0xffffffffu, w.seen);
       w.whole = sg.whole();
-      w.slot = (int(blockIdx.x) * 2 + (sg.k0 == 0 ? 1 : 0)) * kTileR + x * 128 + r;
+      w.slot = part_slot(blockIdx.x, sg.k0) * kTileR + x * 128 + r;
       return true;
     };
     // O and the row in the workspace (see kSumTiles; its reference in part_ml): both
@@ -1419,7 +1244,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         if (whole) {
           store_row8<DT>(p, a, d0, acc, top, sum);
         } else {
-          const int64_t slot = (int64_t(blockIdx.x) * 2 + (cs.k0 == 0 ? 1 : 0)) * L::kR + mt * 16 + r;
+          const int64_t slot = int64_t(part_slot(blockIdx.x, cs.k0)) * L::kR + mt * 16 + r;
           float4* to = reinterpret_cast<float4*>(p.part_o + slot * D + d0);
           to[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
           to[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
@@ -1466,22 +1291,15 @@ __global__ void __launch_bounds__(2 * JoinShape<R>::kHalf, 4) join_kernel(const 
   ItemPlace item = {0, 0, 0};
   int c0 = 0, n = 0;                            // the shares that may hold a part
   bool work = s.u0 != s.u1;
+  if (work) work = cut_item(p, s, k, seg);
   if (work) {
-    const Share::Place& at = k ? s.last : s.first;
-    seg.e = at.e;
-    seg.x = at.x;
-    seg.find(p, at.base, k ? s.u1 - 1 : s.u0);
     item = seg.at;
-    if (item.from >= s.u0 && item.to <= s.u1) work = false;             // all of it is here
-    if (k == 1 && s.u0 >= item.from) work = false;                       // the first half's item too
-  }
-  if (work) {
     c0 = s.holder(item.from);
     n = s.holder(item.to - 1) - c0 + 1;
-    for (int q = tid; q < n; q += kHalf) {       // share c0 + q's key tiles [k0, k1) of the item
-      const int k0 = item.tile_at<KT>(p, max(item.from, s.begin(c0 + q)));
-      const int k1 = item.tile_at<KT>(p, min(item.to, s.begin(c0 + q + 1)));
-      part_row[q] = k0 < k1 ? ((c0 + q) * 2 + (k0 == 0 ? 1 : 0)) * R : -1;
+    for (int q = tid; q < n; q += kHalf) {       // share c0 + q's part
+      int k0, k1;
+      part_of<KT>(item, s, c0 + q, k0, k1);
+      part_row[q] = k0 < k1 ? part_slot(c0 + q, k0) * R : -1;
       if (k0 == 0 && k1 == item.key_tiles) whole[k] = 1;
     }
   }

@@ -864,7 +864,8 @@ def vark_paged_attention(q, cu_tokens, k_pages, v_pages, page_table, cache_len, 
     """Device: attention of a chunk's queries over the paged cache (see vark.h).
     q, out [tokens][Hq][D] with any strides but the channels'; pools, tables and
     lengths as vark_paged_append; tau fp32 [Hq] or None; lse fp32 [tokens][Hq]
-    or None; workspace uint8 of vark_paged_attention_workspace bytes."""
+    or None; workspace uint8 of vark_paged_attention_workspace bytes.  A long
+    chunk among sequences that decode is faster in a call of its own."""
     quick = _quick_module or _quick()
     if quick:
         rc = quick.attention(q, cu_tokens, k_pages, v_pages, page_table, cache_len, tau, causal, out, lse, workspace,

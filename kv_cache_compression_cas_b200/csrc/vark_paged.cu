@@ -21,11 +21,13 @@
 namespace vark {
 namespace paged {
 
-// Both kernels are bound by HBM at large sizes and by one chain of dependent
-// loads (position -> cosines) at small ones: the position is asked for before
+// Both kernels are bound by HBM at large sizes, by one chain of dependent loads
+// (position -> cosines) at small ones and, in between, by the latency of the rows'
+// loads, too few of which are in flight (8 ragged chunks of 79 MB: 17 us, DRAM at
+// 28%): the position is asked for before
 // the rows, rows are read and written as streams, and blocks are small so that
 // a finished one makes room at once.  Measured on the last scale of a batch of
-// 8 (32768 tokens of 16 + 16 heads of 128): 92 us, 5.83 TB/s; 128-thread blocks
+// 8 (32768 tokens of 16 + 16 heads of 128): 92 to 98 us, 5.5 to 5.8 TB/s; 128-thread blocks
 // 100, the position after the rows 111 with plain stores, 8 heads a warp 105.
 constexpr int kRowThreads = 64;
 
@@ -243,8 +245,8 @@ VARK_DEV int find_sequence(const int32_t* cu, int B, int64_t token, int lane) {
 
 constexpr int kKvHeads = 8;        // heads of a warp's token
 
-// 12 blocks an SM (80 registers): 46.1 us for 4 x 4096 tokens of 16 heads into
-// head pages (5.8 TB/s); unbounded (91 registers) 47.5, 4 heads a warp 50.  L2
+// 12 blocks an SM (80 registers): 46 to 48.6 us for 4 x 4096 tokens of 16 heads
+// into head pages (5.5 to 5.8 TB/s); unbounded (91 registers) 47.5, 4 heads a warp 50.  L2
 // prefetches ahead of the wait: 51 (ragged chunks of 79 MB 15.6 instead of 16.5).
 template <int DT, int D>
 __global__ void __launch_bounds__(kRowThreads, 12) append_kernel(const __grid_constant__ AppendParams p) {

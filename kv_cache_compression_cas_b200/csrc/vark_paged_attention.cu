@@ -229,10 +229,10 @@ VARK_DEV void store_row8(const AttnParams& p, const RowAt& a, int d0, const floa
 // The MMA warp runs its loop with all lanes and only predicates the MMAs:
 // descriptors and addresses then stay warp-uniform.
 //
-// Measured (32 heads of 128 over 8 kv heads, bf16): a chunk of 2048 tokens over
-// 16384 cached rows 498 us, 1.17 PFLOP/s, while the clock holds, 567 us (1.03)
-// call after call at the power limit; 8 prompts of 333 to 4099 tokens 443 to
-// 499 us.  A pair of tiles takes 3500 cycles for 128 keys: 2050 of MMAs, whose
+// Measured (32 heads of 128 over 8 kv heads, bf16), call after call, at the power
+// limit: a chunk of 2048 tokens over 16384 cached rows 566 to 585 us, 1.0
+// PFLOP/s; 8 prompts of 333 to 4099 tokens 501 to 512 us (one call after a rest,
+// while the clock holds: 503 and 478).  A pair of tiles takes 3500 cycles for 128 keys: 2050 of MMAs, whose
 // S products read 128 B/clk of shared memory, and as much of exp2 on the two
 // softmax warps of an SM quarter.  What ties them is S -> softmax -> PV -> S.
 // Keys in halves with S a half ahead cut that chain and cost 535 and 495 us:
@@ -575,7 +575,8 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         for (int q = 0; q < 4; ++q) {
           const RowAt row = row_at(p, sg, x * 128 + q * 32 + lane);
           const float tau = p.tau != nullptr && row.token >= 0 ? p.tau[row.head] : 1.f;
-          const int64_t off = row.token < 0 || p.scale_log2 * tau == 0.f ? -1 : row.token * p.qs[0] + row.head * p.qs[1];
+          const bool none = row.token < 0 || p.scale_log2 * tau == 0.f;
+          const int64_t off = none ? -1 : row.token * p.qs[0] + row.head * p.qs[1];
           turned |= tau < 0.f;
 #pragma unroll 4
           for (int it = 0; it < 32 / kRowsAt; ++it) {
@@ -878,13 +879,14 @@ tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
 // tcgen05 tile would be one eighth full.
 //
 // Measured (32 heads of 128 over 8 kv heads, bf16): 64 sequences of up to 8190
-// rows out of 16-row pages 191 us with its join, 6.3 TB/s; one of 65536 rows
+// rows out of 16-row pages 191 to 206 us with its join, 5.8 to 6.3 TB/s; one of 65536 rows
 // 49 us, 5.5 TB/s, of which 7 are finding the share, the handoff and the join.
 // 3 to 7 drafted tokens of 24 heads of 64 for each of 32 caches of up to 4000 rows
 // 46 us, 3.2 TB/s: 12 us do not shrink with the caches (plan, first loads, items'
 // starts and ends, join), and 6 or 7 tokens are two row tiles that read the keys
 // twice; each further row costs what 6.2 TB/s take.  Two key tiles at a time in
-// a warp: 49 us.
+// a warp: 49 us.  A warp's sum takes an eighth of a share's keys, so what an MMA
+// cuts off (see kSumTiles) is 0.1% over 2^20 keys of equal weight.
 // (Warps 0-3 are the loader's group; three of them only hand their registers on.)
 constexpr int kRowWarps = 8;
 constexpr int kRowThreads = kRowWarps * 32 + 128;
@@ -1399,6 +1401,10 @@ __global__ void __launch_bounds__(2 * JoinShape<R>::kHalf, 4) join_kernel(const 
 // on tcgen05); up to 32 two (20 rows: 31, 33 as one at a time, 42); D = 64 two
 // at a time up to 64 (64 rows: 32 against 35 on tcgen05, 96: 41 against 34);
 // beyond that 256 on tcgen05 (D = 128, 48 rows: 43 against 45; 96: 44 against 59).
+// All of these were batches of sequences with about as many tokens each.  A chunk
+// among sequences that decode goes the mean's way, which is slow for it: 255 of
+// one token and one of 1700 over caches of 3000 rows 1059 us in one call, 618 as
+// two; 63 and one of 2048 293 and 290.
 static int choose_rows(int64_t n_tokens, int B, int Hq, int Hkv, int D) {
   const int64_t rows = n_tokens * (Hq / Hkv);         // of a kv head, over all sequences
   return rows <= int64_t(B) * 16 ? 16 : rows <= int64_t(B) * (D == 64 ? 64 : 32) ? 32 : kTileR;
